@@ -1,0 +1,577 @@
+// ops.cu -- the serving operators of include/m3_ops.h that move and count:
+// page tables and slot maps, the K/V store, rules on logits.  The attention
+// operators are in ops_attn.cu.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <string>
+
+#include "common.cuh"
+#include "m3_ops.h"
+#include "ops.cuh"
+
+namespace m3 {
+
+namespace {
+
+// ------------------------------------------------------------------- map ---
+// Every CTA scans the request lengths by itself (8 + 4 bytes a request, at
+// most 96 KB from L2), so the map is one launch without a wait between CTAs:
+// the table columns that the scan gives out are written by one CTA and read by
+// none, since a token's page is taken from the free list by the same sum.
+// The columns of the cached tokens are read only.
+constexpr int kMapThreads = 512;
+constexpr int kMapMaxReq = 8192;
+
+struct MapArgs {
+  const int32_t *fresh, *cached, *free_pages, *free_at;
+  int32_t* table;
+  int32_t *cu, *positions, *seqs, *lens, *taken;
+  int64_t* slots;
+  int64_t ld_table;
+  int n_req, n_free, max_pages, shift, n_pages, start, n_tokens;
+};
+
+__device__ __forceinline__ int sat(long long v) { return v > INT_MAX ? INT_MAX : (int)v; }
+
+__device__ __forceinline__ int free_page(const MapArgs& a, long long i) {
+  if (i < 0 || i >= a.n_free) return -1;
+  const int p = a.free_pages[i];
+  return p >= 0 && p < a.n_pages ? p : -1;
+}
+
+__global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
+  extern __shared__ int map_smem[];
+  int* scu = map_smem;                // [n_req + 1] first token of each request
+  int* soff = map_smem + a.n_req + 1;  // [n_req] pages given out before it
+  __shared__ long long warp_tok[kMapThreads / 32], warp_pg[kMapThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int p1 = (1 << a.shift) - 1;
+  // each thread's run of requests, then a scan over the threads (64-bit sums)
+  const int per = (a.n_req + kMapThreads - 1) / kMapThreads;
+  const int r0 = min(a.n_req, tid * per), r1 = min(a.n_req, r0 + per);
+  auto load = [&](int r, int& f, int& c, int& want) {
+    f = max(0, a.fresh[r]);
+    c = a.cached ? max(0, a.cached[r]) : 0;
+    const long long have = ((long long)c + p1) >> a.shift;
+    const long long need = ((long long)c + f + p1) >> a.shift;
+    want = (int)max(0ll, min(need, (long long)a.max_pages) - have);
+  };
+  long long tok = 0, pg = 0;
+  for (int r = r0; r < r1; ++r) {
+    int f, c, w;
+    load(r, f, c, w);
+    tok += f;
+    pg += w;
+  }
+  long long it = tok, ip = pg;  // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(~0u, it, o), p = __shfl_up_sync(~0u, ip, o);
+    if (lane >= o) {
+      it += t;
+      ip += p;
+    }
+  }
+  if (lane == 31) {
+    warp_tok[warp] = it;
+    warp_pg[warp] = ip;
+  }
+  __syncthreads();
+  long long bt = it - tok, bp = ip - pg, all_tok = 0, all_pg = 0;
+  for (int w = 0; w < kMapThreads / 32; ++w) {
+    if (w < warp) {
+      bt += warp_tok[w];
+      bp += warp_pg[w];
+    }
+    all_tok += warp_tok[w];
+    all_pg += warp_pg[w];
+  }
+  for (int r = r0; r < r1; ++r) {
+    int f, c, w;
+    load(r, f, c, w);
+    scu[r] = sat(bt);
+    soff[r] = sat(bp);
+    bt += f;
+    bp += w;
+    if (blockIdx.x == 0) {
+      a.cu[r] = scu[r];
+      a.lens[r] = sat((long long)c + f);
+    }
+  }
+  if (tid == 0) {
+    scu[a.n_req] = sat(all_tok);
+    if (blockIdx.x == 0) {
+      a.cu[a.n_req] = sat(all_tok);
+      *a.taken = sat(all_pg);
+    }
+  }
+  __syncthreads();
+  const int first = a.free_at ? max(0, *a.free_at) : 0;
+
+  // the new table columns: one warp per request
+  const int nwarps = gridDim.x * (kMapThreads / 32);
+  for (int r = blockIdx.x * (kMapThreads / 32) + warp; r < a.n_req; r += nwarps) {
+    int f, c, w;
+    load(r, f, c, w);
+    if (w == 0) continue;
+    int32_t* row = a.table + r * a.ld_table + (((long long)c + p1) >> a.shift);
+    for (int i = lane; i < w; i += 32) row[i] = free_page(a, (long long)first + soff[r] + i);
+  }
+
+  // the tokens: four in a row per thread, so that the three maps leave in
+  // 16-byte stores
+  const int total = min(scu[a.n_req], a.n_tokens);
+  const long long step = 4ll * gridDim.x * kMapThreads;
+  for (long long t0 = 4ll * (blockIdx.x * kMapThreads + tid); t0 < a.n_tokens; t0 += step) {
+    int pos[4], seq[4];
+    long long slot[4];
+    int lo = 0;
+    if (t0 < total) {  // the last request that starts at or before t0
+      int hi = a.n_req - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (scu[mid] <= t0) lo = mid;
+        else hi = mid - 1;
+      }
+    }
+    int of = -1, f = 0, c = 0, w = 0;  // the request whose lengths are loaded
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long t = t0 + i;
+      pos[i] = seq[i] = -1;
+      slot[i] = -1;
+      if (t >= total) continue;
+      while (scu[lo + 1] <= t) ++lo;
+      if (lo != of) {
+        load(lo, f, c, w);
+        of = lo;
+      }
+      const long long j = (long long)c + (t - scu[lo]);  // place in the request's table
+      seq[i] = lo;
+      pos[i] = sat(a.start + j);
+      const long long col = j >> a.shift, have = ((long long)c + p1) >> a.shift;
+      int page = -1;
+      if (col < a.max_pages) {
+        if (col >= have) {
+          page = free_page(a, (long long)first + soff[lo] + (col - have));
+        } else {
+          page = a.table[lo * a.ld_table + col];
+          if (page >= a.n_pages) page = -1;
+        }
+      }
+      if (page >= 0) slot[i] = ((long long)page << a.shift) | (j & p1);
+    }
+    if (t0 + 4 <= a.n_tokens) {
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.seqs + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < a.n_tokens) {
+          a.positions[t0 + i] = pos[i];
+          a.seqs[t0 + i] = seq[i];
+          a.slots[t0 + i] = slot[i];
+        }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- store ---
+// 16-byte pieces: a thread keeps one (K or V, head, piece) column and walks
+// tokens, four loads in flight; VEC = false: sources whose rows are not
+// 16-byte aligned, read in 16-bit words.
+constexpr int kStoreThreads = 256;
+constexpr int kStoreUnroll = 4;
+
+struct StoreArgs {
+  const uint16_t *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  const int64_t* slots;
+  uint4* pool;
+  long long n_slots;
+  int n_tokens, Hkv, pieces, shift;
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs a) {
+  const int ncol = 2 * a.Hkv * a.pieces;
+  // threads of a block: `groups` tokens side by side, each over the columns
+  const int width = min(ncol, kStoreThreads), groups = kStoreThreads / width;
+  const int g = threadIdx.x / width;
+  if (g >= groups) return;
+  const long long page_pieces = (long long)ncol << a.shift;
+  for (int col = threadIdx.x % width; col < ncol; col += width) {
+    const int hv = col / a.pieces, piece = col % a.pieces;  // head slot (K heads, V heads)
+    const bool isv = hv >= a.Hkv;
+    const uint16_t* src = isv ? a.v + (hv - a.Hkv) * a.v_head : a.k + hv * a.k_head;
+    const int64_t st = isv ? a.v_token : a.k_token;
+    const long long step = (long long)gridDim.x * groups;
+    for (long long t0 = (long long)blockIdx.x * groups + g; t0 < a.n_tokens;
+         t0 += step * kStoreUnroll) {
+      uint4 val[kStoreUnroll];
+      long long slot[kStoreUnroll];
+#pragma unroll
+      for (int u = 0; u < kStoreUnroll; ++u) {
+        const long long t = t0 + u * step;
+        slot[u] = t < a.n_tokens ? a.slots[t] : -1;
+        if (slot[u] >= a.n_slots) slot[u] = -1;
+        if (slot[u] >= 0) {
+          const uint16_t* p = src + t * st + piece * 8;
+          if constexpr (VEC) {
+            val[u] = __ldg(reinterpret_cast<const uint4*>(p));
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+            val[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kStoreUnroll; ++u)
+        if (slot[u] >= 0) {
+          const long long page = slot[u] >> a.shift, off = slot[u] & ((1ll << a.shift) - 1);
+          a.pool[page * page_pieces + (((long long)hv << a.shift) + off) * a.pieces + piece] =
+              val[u];
+        }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- rules ---
+// A CTA takes a run of one row's vocabulary.  It counts the row's history
+// tokens that fall in the run in shared memory (whole numbers: the order of
+// the atomics does not matter), puts the run's biases beside the counts, then
+// streams the logits once: read, rules, write.
+constexpr int kRuleThreads = 256;
+constexpr int kRuleMaxBias = 4096;
+
+struct RuleArgs {
+  const void* in;
+  void* out;
+  int64_t ld_in, ld_out;
+  const int32_t* history;
+  int64_t ld_history;
+  const int32_t* hist_len;
+  const float *rep, *freq, *pres;
+  const int32_t* bias_ids;
+  const float* bias;
+  const uint32_t* mask;
+  const int32_t* mask_row;
+  int vocab, n_history, n_bias, n_masks, words, run, runs;
+};
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f(float v) { return v; }
+template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+
+template <typename T>
+__global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const RuleArgs a) {
+  constexpr int VEC = 16 / sizeof(T);
+  extern __shared__ int rule_smem[];
+  const int tid = threadIdx.x;
+  const int row = blockIdx.x / a.runs, part = blockIdx.x % a.runs;
+  const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
+  T* out = static_cast<T*>(a.out) + row * a.ld_out;
+  // runs start on a 16-byte boundary of the row, so the first may be short
+  const int lead = (int)((reinterpret_cast<uintptr_t>(in) / sizeof(T)) % VEC);
+  const bool vec_out = (reinterpret_cast<uintptr_t>(out) / sizeof(T)) % VEC == (unsigned)lead;
+  const long long s0 = (long long)part * a.run - lead;
+  const int lo = (int)max(s0, 0ll), hi = (int)min(s0 + a.run, (long long)a.vocab);
+  if (lo >= hi) return;
+  const bool counts = a.history != nullptr, biases = a.n_bias > 0;
+  int* cnt = rule_smem;                       // [run] times in the history
+  int* badd = rule_smem + (counts ? a.run : 0);  // [run] the bias, as float bits
+  const int used = (counts ? a.run : 0) + (biases ? a.run : 0);
+  for (int i = tid * 4; i < used; i += kRuleThreads * 4)
+    *reinterpret_cast<int4*>(rule_smem + i) = make_int4(0, 0, 0, 0);
+  if (used) __syncthreads();
+
+  if (counts) {
+    const int32_t* h = a.history + row * a.ld_history;
+    int n = a.n_history;
+    if (a.hist_len) n = min(n, max(0, a.hist_len[row]));
+    auto add = [&](int id) {
+      if (id >= lo && id < hi) atomicAdd(&cnt[(int)(id - s0)], 1);
+    };
+    if ((reinterpret_cast<uintptr_t>(h) & 15) == 0) {
+      const int n4 = n >> 2;
+#pragma unroll 4
+      for (int i = tid; i < n4; i += kRuleThreads) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(h) + i);
+        add(v.x);
+        add(v.y);
+        add(v.z);
+        add(v.w);
+      }
+      for (int i = (n4 << 2) + tid; i < n; i += kRuleThreads) add(h[i]);
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kRuleThreads) add(h[i]);
+    }
+  }
+  if (biases) {
+    // the first entry of each token owns it: its place is kept as n_bias - e
+    // (a maximum, whatever the order); it adds up the token's entries in
+    // their order, looking past itself only where some token came twice
+    __shared__ int twice;
+    const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
+    const float* val = a.bias + (size_t)row * a.n_bias;
+    if (tid == 0) twice = 0;
+    for (int e = tid; e < a.n_bias; e += kRuleThreads) {
+      const int id = ids[e];
+      if (id >= lo && id < hi) atomicMax(&badd[(int)(id - s0)], a.n_bias - e);
+    }
+    __syncthreads();
+    uint32_t mine = 0;
+    for (int e = tid, i = 0; e < a.n_bias; e += kRuleThreads, ++i) {
+      const int id = ids[e];
+      if (id >= lo && id < hi) {
+        if (badd[(int)(id - s0)] == a.n_bias - e) mine |= 1u << i;
+        else twice = 1;
+      }
+    }
+    __syncthreads();
+    const bool look = twice != 0;
+    for (int e = tid, i = 0; e < a.n_bias; e += kRuleThreads, ++i)
+      if ((mine >> i) & 1) {
+        const int id = ids[e];
+        float b = val[e];
+        if (look)
+          for (int f = e + 1; f < a.n_bias; ++f)
+            if (ids[f] == id) b += val[f];
+        badd[(int)(id - s0)] = __float_as_int(b);
+      }
+  }
+  if (used) __syncthreads();
+
+  const float rep = a.rep ? a.rep[row] : 1.0f, freq = a.freq ? a.freq[row] : 0.0f;
+  const float pres = a.pres ? a.pres[row] : 0.0f;
+  const uint32_t* mask = nullptr;
+  if (a.mask) {
+    const int m = a.mask_row ? a.mask_row[row] : (a.n_masks == 1 ? 0 : row);
+    if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * a.words;
+  }
+  auto rule = [&](float x, int c, float b, bool allowed) -> float {
+    if (c > 0) {
+      x = x > 0.0f ? x / rep : x * rep;
+      x -= freq * (float)c;
+      x -= pres;
+    }
+    if (biases) x += b;  // 0 where the token has none: x stays
+    return allowed ? x : -INFINITY;
+  };
+  for (int j = tid * VEC; j < a.run; j += kRuleThreads * VEC) {
+    const long long i0 = s0 + j;
+    if (i0 + VEC <= lo || i0 >= hi) continue;
+    if (i0 >= lo && i0 + VEC <= hi) {
+      uint4 raw = *reinterpret_cast<const uint4*>(in + i0);
+      T x[VEC];
+      *reinterpret_cast<uint4*>(x) = raw;
+      uint32_t bits = ~0u;  // of i0, i0 + 1, ...
+      if (mask) {
+        const int w = (int)(i0 >> 5), s = (int)(i0 & 31);
+        const uint32_t w0 = __ldg(mask + w);
+        const uint32_t w1 = s + VEC > 32 ? __ldg(mask + w + 1) : 0u;
+        bits = __funnelshift_r(w0, w1, s);
+      }
+#pragma unroll
+      for (int q = 0; q < VEC; q += 4) {
+        int4 c = make_int4(0, 0, 0, 0), b = c;
+        if (counts) c = *reinterpret_cast<const int4*>(cnt + j + q);
+        if (biases) b = *reinterpret_cast<const int4*>(badd + j + q);
+        x[q] = from_f<T>(rule(to_f(x[q]), c.x, __int_as_float(b.x), (bits >> q) & 1));
+        x[q + 1] = from_f<T>(rule(to_f(x[q + 1]), c.y, __int_as_float(b.y), (bits >> (q + 1)) & 1));
+        x[q + 2] = from_f<T>(rule(to_f(x[q + 2]), c.z, __int_as_float(b.z), (bits >> (q + 2)) & 1));
+        x[q + 3] = from_f<T>(rule(to_f(x[q + 3]), c.w, __int_as_float(b.w), (bits >> (q + 3)) & 1));
+      }
+      if (vec_out) {
+        *reinterpret_cast<uint4*>(out + i0) = *reinterpret_cast<const uint4*>(x);
+      } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) out[i0 + q] = x[q];
+      }
+    } else {
+      for (int q = 0; q < VEC; ++q) {
+        const long long i = i0 + q;
+        if (i < lo || i >= hi) continue;
+        const bool ok = !mask || ((__ldg(mask + (i >> 5)) >> (i & 31)) & 1);
+        out[i] = from_f<T>(rule(to_f(in[i]), counts ? cnt[j + q] : 0,
+                                biases ? __int_as_float(badd[j + q]) : 0.0f, ok));
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_rules(const RuleArgs& a, int n_rows, cudaStream_t st) {
+  const size_t smem = sizeof(int) * a.run * ((a.history ? 1 : 0) + (a.n_bias > 0 ? 1 : 0));
+  logit_rules_kernel<T><<<(unsigned)(n_rows * a.runs), kRuleThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int page_shift(int page) {
+  if (page < 16 || page > 1024 || (page & (page - 1))) return -1;
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
+int sm_count() {
+  static thread_local int dev_of = -1, n = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev != dev_of) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    dev_of = dev;
+  }
+  return n;
+}
+
+}  // namespace m3
+
+using namespace m3;
+
+#define OPS_CK(call)                                                                  \
+  do {                                                                                \
+    const cudaError_t e_ = (call);                                                    \
+    if (e_ != cudaSuccess)                                                            \
+      return set_error(M3_ECUDA, std::string(#call) + ": " + cudaGetErrorString(e_)); \
+  } while (0)
+
+extern "C" int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
+                         const int32_t* free_pages, int n_free, const int32_t* free_at,
+                         int32_t* table, int max_pages, int64_t ld_table, int page, int n_pages,
+                         int start, int n_tokens, int32_t* cu, int32_t* positions, int64_t* slots,
+                         int32_t* seqs, int32_t* lens, int32_t* taken, void* cuda_stream) {
+  if (n_req < 1 || n_req > kMapMaxReq) return set_error(M3_EINVAL, "n_req out of 1..8192");
+  const int shift = page_shift(page);
+  if (shift < 0) return set_error(M3_EINVAL, "page: a power of two, 16..1024");
+  if (n_free < 0 || max_pages < 0 || n_pages < 0 || n_tokens < 0 || start < 0)
+    return set_error(M3_EINVAL, "negative count");
+  if (ld_table < max_pages) return set_error(M3_EINVAL, "ld_table < max_pages");
+  if (!fresh || !cu || !lens || !taken || (n_free && !free_pages) || (max_pages && !table) ||
+      (n_tokens && (!positions || !slots || !seqs)))
+    return set_error(M3_EINVAL, "null argument");
+  if (free_at == taken) return set_error(M3_EINVAL, "free_at and taken are the same word");
+  if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots) |
+       reinterpret_cast<uintptr_t>(seqs)) & 15)
+    return set_error(M3_EINVAL, "positions, slots and seqs have to be 16-byte aligned");
+  MapArgs a{fresh, cached, free_pages, free_at, table, cu, positions, seqs, lens, taken, slots,
+            ld_table, n_req, n_free, max_pages, shift, n_pages, start, n_tokens};
+  const long long by_tok = (n_tokens + 4ll * kMapThreads - 1) / (4ll * kMapThreads);
+  const long long by_req = (n_req + 63) / 64;  // four requests' columns per warp
+  long long grid = by_tok > by_req ? by_tok : by_req;
+  const int nsm = sm_count();
+  if (grid > 2 * nsm) grid = 2 * nsm;
+  if (grid < 1) grid = 1;
+  const size_t smem = sizeof(int) * (2 * (size_t)n_req + 1);
+  if (smem > 48 * 1024)
+    OPS_CK(cudaFuncSetAttribute(kv_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(sizeof(int) * (2 * (size_t)kMapMaxReq + 1))));
+  kv_map_kernel<<<(unsigned)grid, kMapThreads, smem, static_cast<cudaStream_t>(cuda_stream)>>>(a);
+  OPS_CK(cudaGetLastError());
+  return M3_OK;
+}
+
+extern "C" int m3_kv_store(int dtype, int n_tokens, int Hkv, int D, const void* k, int64_t k_token,
+                           int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                           const int64_t* slots, void* pool, int n_pages, int page,
+                           void* cuda_stream) {
+  if (dtype != M3_KV_BF16 && dtype != M3_KV_F16) return set_error(M3_EINVAL, "dtype");
+  if (n_tokens < 0 || n_pages < 0 || Hkv < 1 || Hkv > 1024)
+    return set_error(M3_EINVAL, "n_tokens, n_pages or Hkv");
+  if (D < 8 || D > 1024 || D % 8) return set_error(M3_EINVAL, "D: a multiple of 8, up to 1024");
+  const int shift = page_shift(page);
+  if (shift < 0) return set_error(M3_EINVAL, "page: a power of two, 16..1024");
+  if (n_tokens == 0 || n_pages == 0) return M3_OK;
+  if (!k || !v || !slots || !pool) return set_error(M3_EINVAL, "null argument");
+  if (reinterpret_cast<uintptr_t>(pool) & 15)
+    return set_error(M3_EINVAL, "the pool has to be 16-byte aligned");
+  StoreArgs a{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_token, k_head,
+              v_token, v_head, slots, static_cast<uint4*>(pool), (long long)n_pages << shift,
+              n_tokens, Hkv, D / 8, shift};
+  const bool vec = !((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) &&
+                   !((k_token | k_head | v_token | v_head) & 7);
+  const int ncol = 2 * Hkv * a.pieces, width = ncol < kStoreThreads ? ncol : kStoreThreads;
+  const long long groups = kStoreThreads / width;
+  long long grid = (n_tokens + groups - 1) / groups;
+  const long long most = 8ll * sm_count();
+  if (grid > most) grid = most;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (vec) kv_store_kernel<true><<<(unsigned)grid, kStoreThreads, 0, st>>>(a);
+  else kv_store_kernel<false><<<(unsigned)grid, kStoreThreads, 0, st>>>(a);
+  OPS_CK(cudaGetLastError());
+  return M3_OK;
+}
+
+extern "C" int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logits,
+                              int64_t ld_logits, void* out, int64_t ld_out, const int32_t* history,
+                              int n_history, int64_t ld_history, const int32_t* hist_len,
+                              const float* repetition, const float* frequency,
+                              const float* presence, const int32_t* bias_ids, const float* bias,
+                              int n_bias, const uint32_t* mask, int n_masks,
+                              const int32_t* mask_row, void* cuda_stream) {
+  if (dtype != M3_LOGITS_F32 && dtype != M3_LOGITS_BF16 && dtype != M3_LOGITS_F16)
+    return set_error(M3_EINVAL, "dtype");
+  if (n_rows < 0 || vocab < 1 || vocab > (1 << 30)) return set_error(M3_EINVAL, "n_rows or vocab");
+  if (n_history < 0 || n_bias < 0 || n_bias > kRuleMaxBias || n_masks < 0)
+    return set_error(M3_EINVAL, "n_history, n_bias (up to 4096) or n_masks");
+  if (n_rows == 0) return M3_OK;
+  if (!logits || !out) return set_error(M3_EINVAL, "null argument");
+  if (n_bias && (!bias_ids || !bias)) return set_error(M3_EINVAL, "null bias_ids or bias");
+  if (n_history && !history) return set_error(M3_EINVAL, "null history");
+  if (mask && n_masks < 1) return set_error(M3_EINVAL, "a mask without n_masks");
+  if (mask && !mask_row && n_masks != 1 && n_masks != n_rows)
+    return set_error(M3_EINVAL, "without mask_row, n_masks is 1 or n_rows");
+  if (n_rows > 1 && (ld_logits < vocab || ld_out < vocab || (n_history && ld_history < n_history)))
+    return set_error(M3_EINVAL, "rows overlap");
+  const int es = dtype == M3_LOGITS_F32 ? 4 : 2;
+  const uintptr_t i0 = reinterpret_cast<uintptr_t>(logits), o0 = reinterpret_cast<uintptr_t>(out);
+  if ((i0 | o0) & (es - 1)) return set_error(M3_EINVAL, "logits or out not aligned to their type");
+  const uintptr_t ni = ((uintptr_t)(n_rows - 1) * ld_logits + vocab) * es;
+  const uintptr_t no = ((uintptr_t)(n_rows - 1) * ld_out + vocab) * es;
+  const bool same = i0 == o0 && (n_rows == 1 || ld_logits == ld_out);
+  if (!same && i0 < o0 + no && o0 < i0 + ni)
+    return set_error(M3_EINVAL, "out overlaps logits without being logits");
+  RuleArgs a{};
+  a.in = logits;
+  a.out = out;
+  a.ld_in = ld_logits;
+  a.ld_out = ld_out;
+  a.history = n_history ? history : nullptr;
+  a.ld_history = ld_history;
+  a.hist_len = hist_len;
+  a.rep = repetition;
+  a.freq = frequency;
+  a.pres = presence;
+  a.bias_ids = bias_ids;
+  a.bias = bias;
+  a.mask = mask;
+  a.mask_row = mask_row;
+  a.vocab = vocab;
+  a.n_history = n_history;
+  a.n_bias = n_bias;
+  a.n_masks = n_masks;
+  a.words = (vocab + 31) / 32;
+  // a run: 4096 logits, or 1024 where those would leave SMs without a CTA
+  const long long big = ((long long)vocab + 7 + 4095) / 4096;
+  a.run = big * n_rows < 2ll * sm_count() ? 1024 : 4096;
+  a.runs = (int)(((long long)vocab + 7 + a.run - 1) / a.run);
+  if ((long long)a.runs * n_rows > INT_MAX) return set_error(M3_EINVAL, "too many rows");
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (dtype == M3_LOGITS_F32) OPS_CK(launch_rules<float>(a, n_rows, st));
+  else if (dtype == M3_LOGITS_BF16) OPS_CK(launch_rules<__nv_bfloat16>(a, n_rows, st));
+  else OPS_CK(launch_rules<__half>(a, n_rows, st));
+  return M3_OK;
+}
