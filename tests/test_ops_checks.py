@@ -8,8 +8,22 @@ import torch
 from test_abi import _declared
 
 
+VP, I32, I64, F32 = C.c_void_p, C.c_int, C.c_int64, C.c_float
+ARGS = {
+    "m3_kv_map": [I32, VP, VP, VP, I32, VP, VP, I32, I64, I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, VP],
+    "m3_kv_store": [I32, I32, I32, I32, VP, I64, I64, VP, I64, I64, VP, VP, I32, I32, VP],
+    "m3_attn_prompt": [I32, I32, I32, I32, I32, I32, I32, VP, I64, I64, VP, I64, I64, VP, I64, I64, VP, VP, F32, VP,
+                       I64, I64, VP, VP],
+    "m3_attn_prefix": [I32, I32, I32, I32, I32, VP, I64, I64, VP, I32, I32, VP, I32, I32, VP, I32, I64, VP, F32, VP,
+                       I64, I64, VP, VP, I64, VP],
+    "m3_logit_rules": [I32, I32, I32, VP, I64, VP, I64, VP, I32, I64, VP, VP, VP, VP, VP, VP, I32, VP, I32, VP, VP],
+}
+
+
 def _lib():
     from autoregressive_audio_token_b200 import m3, ops
+    for name, args in ARGS.items():
+        getattr(m3.lib, name).argtypes = args
     return m3, ops, m3.lib
 
 
