@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs
 #pragma unroll
       for (int u = 0; u < kStoreUnroll; ++u) {
         const long long t = t0 + u * step;
-        slot[u] = t < a.n_tokens ? a.slots[t] : -1;
-        if (slot[u] >= a.n_slots) slot[u] = -1;
-        if (slot[u] >= 0) {
-          const uint16_t* p = src + t * st + piece * 8;
+        slot[u] = -1;
+        if (t < a.n_tokens) {
+          slot[u] = __ldg(a.slots + t);
+          const uint16_t* p = src + t * st + piece * 8;  // read whatever the slot says
           if constexpr (VEC) {
             val[u] = __ldg(reinterpret_cast<const uint4*>(p));
           } else {
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs
             for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
             val[u] = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          if (slot[u] >= a.n_slots) slot[u] = -1;
         }
       }
 #pragma unroll
@@ -242,12 +243,17 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs
 }
 
 // ----------------------------------------------------------------- rules ---
-// A CTA takes a run of one row's vocabulary.  It counts the row's history
-// tokens that fall in the run in shared memory (whole numbers: the order of
-// the atomics does not matter), puts the run's biases beside the counts, then
-// streams the logits once: read, rules, write.
-constexpr int kRuleThreads = 256;
-constexpr int kRuleMaxBias = 4096;
+// A CTA takes a run of one row's vocabulary.  It asks for its logits first;
+// while they come it notes in one word of shared memory per token how often
+// the row's history has it (whole numbers: the order of the atomics does not
+// matter) and which bias entry is its own; then the rules, from registers, and
+// one write.  Few tokens have a word other than 0, so most pieces only meet
+// the mask.  Every run of a row reads the whole history again, so runs are
+// long.
+constexpr int kRuleThreads = 512;
+constexpr int kRuleRun = 8192;  // logits of the longest run
+constexpr int kCountBits = 19;  // of the word: the count; above it the bias entry's code
+constexpr int kRuleMaxBias = 4095, kRuleMaxHistory = (1 << kCountBits) - 1;
 
 struct RuleArgs {
   const void* in;
@@ -274,8 +280,9 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 
 template <typename T>
-__global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const RuleArgs a) {
+__global__ void __launch_bounds__(kRuleThreads, 2) logit_rules_kernel(const RuleArgs a) {
   constexpr int VEC = 16 / sizeof(T);
+  constexpr int KV = kRuleRun / (VEC * kRuleThreads);  // 16-byte pieces per thread
   extern __shared__ int rule_smem[];
   const int tid = threadIdx.x;
   const int row = blockIdx.x / a.runs, part = blockIdx.x % a.runs;
@@ -287,24 +294,70 @@ __global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const RuleArg
   const long long s0 = (long long)part * a.run - lead;
   const int lo = (int)max(s0, 0ll), hi = (int)min(s0 + a.run, (long long)a.vocab);
   if (lo >= hi) return;
-  const bool counts = a.history != nullptr, biases = a.n_bias > 0;
-  int* cnt = rule_smem;                       // [run] times in the history
-  int* badd = rule_smem + (counts ? a.run : 0);  // [run] the bias, as float bits
-  const int used = (counts ? a.run : 0) + (biases ? a.run : 0);
-  for (int i = tid * 4; i < used; i += kRuleThreads * 4)
-    *reinterpret_cast<int4*>(rule_smem + i) = make_int4(0, 0, 0, 0);
-  if (used) __syncthreads();
-
+  uint4 raw[KV];
+#pragma unroll
+  for (int u = 0; u < KV; ++u) {
+    const int j = (u * kRuleThreads + tid) * VEC;
+    if (j < a.run && s0 + j >= lo && s0 + j + VEC <= hi)
+      raw[u] = *reinterpret_cast<const uint4*>(in + s0 + j);
+  }
+  const float rep = a.rep ? __ldg(a.rep + row) : 1.0f, freq = a.freq ? __ldg(a.freq + row) : 0.0f;
+  const float pres = a.pres ? __ldg(a.pres + row) : 0.0f;
+  const uint32_t* mask = nullptr;
+  if (a.mask) {
+    const int m = a.mask_row ? __ldg(a.mask_row + row) : (a.n_masks == 1 ? 0 : row);
+    if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * a.words;
+  }
+  const bool counts = a.history != nullptr, biases = a.n_bias > 0, noted = counts || biases;
+  int* note = rule_smem;                                       // [run]
+  float* bsum = reinterpret_cast<float*>(rule_smem + a.run);  // [n_bias] of the entries that own a token
+  if (noted) {
+    for (int i = tid * 4; i < a.run; i += kRuleThreads * 4)
+      *reinterpret_cast<int4*>(note + i) = make_int4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  if (biases) {
+    // the first entry of each token owns it: entry e has the code n_bias - e
+    // and the largest stays, whatever the order; the owner adds up the token's
+    // entries in their order, looking past itself only where a token came twice
+    __shared__ int twice;
+    const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
+    const float* val = a.bias + (size_t)row * a.n_bias;
+    if (tid == 0) twice = 0;
+    for (int e = tid; e < a.n_bias; e += kRuleThreads) {
+      const int id = __ldg(ids + e);
+      if (id >= lo && id < hi) {
+        bsum[e] = __ldg(val + e);
+        atomicMax(&note[(int)(id - s0)], (a.n_bias - e) << kCountBits);
+      }
+    }
+    __syncthreads();
+    bool again = false;
+    for (int e = tid; e < a.n_bias; e += kRuleThreads) {
+      const int id = __ldg(ids + e);
+      if (id >= lo && id < hi && note[(int)(id - s0)] >> kCountBits != a.n_bias - e) again = true;
+    }
+    if (again) twice = 1;
+    __syncthreads();
+    if (twice) {
+      for (int e = tid; e < a.n_bias; e += kRuleThreads) {
+        const int id = __ldg(ids + e);
+        if (id >= lo && id < hi && note[(int)(id - s0)] >> kCountBits == a.n_bias - e)
+          for (int f = e + 1; f < a.n_bias; ++f)
+            if (__ldg(ids + f) == id) bsum[e] += __ldg(val + f);
+      }
+    }
+  }
   if (counts) {
     const int32_t* h = a.history + row * a.ld_history;
     int n = a.n_history;
-    if (a.hist_len) n = min(n, max(0, a.hist_len[row]));
+    if (a.hist_len) n = min(n, max(0, __ldg(a.hist_len + row)));
     auto add = [&](int id) {
-      if (id >= lo && id < hi) atomicAdd(&cnt[(int)(id - s0)], 1);
+      if (id >= lo && id < hi) atomicAdd(&note[(int)(id - s0)], 1);
     };
     if ((reinterpret_cast<uintptr_t>(h) & 15) == 0) {
       const int n4 = n >> 2;
-#pragma unroll 4
+#pragma unroll 2
       for (int i = tid; i < n4; i += kRuleThreads) {
         const int4 v = __ldg(reinterpret_cast<const int4*>(h) + i);
         add(v.x);
@@ -312,86 +365,54 @@ __global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const RuleArg
         add(v.z);
         add(v.w);
       }
-      for (int i = (n4 << 2) + tid; i < n; i += kRuleThreads) add(h[i]);
+      for (int i = (n4 << 2) + tid; i < n; i += kRuleThreads) add(__ldg(h + i));
     } else {
 #pragma unroll 4
-      for (int i = tid; i < n; i += kRuleThreads) add(h[i]);
+      for (int i = tid; i < n; i += kRuleThreads) add(__ldg(h + i));
     }
   }
-  if (biases) {
-    // the first entry of each token owns it: its place is kept as n_bias - e
-    // (a maximum, whatever the order); it adds up the token's entries in
-    // their order, looking past itself only where some token came twice
-    __shared__ int twice;
-    const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
-    const float* val = a.bias + (size_t)row * a.n_bias;
-    if (tid == 0) twice = 0;
-    for (int e = tid; e < a.n_bias; e += kRuleThreads) {
-      const int id = ids[e];
-      if (id >= lo && id < hi) atomicMax(&badd[(int)(id - s0)], a.n_bias - e);
-    }
-    __syncthreads();
-    uint32_t mine = 0;
-    for (int e = tid, i = 0; e < a.n_bias; e += kRuleThreads, ++i) {
-      const int id = ids[e];
-      if (id >= lo && id < hi) {
-        if (badd[(int)(id - s0)] == a.n_bias - e) mine |= 1u << i;
-        else twice = 1;
-      }
-    }
-    __syncthreads();
-    const bool look = twice != 0;
-    for (int e = tid, i = 0; e < a.n_bias; e += kRuleThreads, ++i)
-      if ((mine >> i) & 1) {
-        const int id = ids[e];
-        float b = val[e];
-        if (look)
-          for (int f = e + 1; f < a.n_bias; ++f)
-            if (ids[f] == id) b += val[f];
-        badd[(int)(id - s0)] = __float_as_int(b);
-      }
-  }
-  if (used) __syncthreads();
+  if (noted) __syncthreads();
 
-  const float rep = a.rep ? a.rep[row] : 1.0f, freq = a.freq ? a.freq[row] : 0.0f;
-  const float pres = a.pres ? a.pres[row] : 0.0f;
-  const uint32_t* mask = nullptr;
-  if (a.mask) {
-    const int m = a.mask_row ? a.mask_row[row] : (a.n_masks == 1 ? 0 : row);
-    if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * a.words;
-  }
-  auto rule = [&](float x, int c, float b, bool allowed) -> float {
+  // x / repetition as a product with its reciprocal: one more rounding in
+  // fp32, no division per logit
+  const float inv = 1.0f / rep;
+  auto rule = [&](float x, int w) -> float {
+    const int c = w & ((1 << kCountBits) - 1), code = w >> kCountBits;
     if (c > 0) {
-      x = x > 0.0f ? x / rep : x * rep;
+      x = x > 0.0f ? x * inv : x * rep;
       x -= freq * (float)c;
       x -= pres;
     }
-    if (biases) x += b;  // 0 where the token has none: x stays
-    return allowed ? x : -INFINITY;
+    if (code > 0) x += bsum[a.n_bias - code];
+    return x;
   };
-  for (int j = tid * VEC; j < a.run; j += kRuleThreads * VEC) {
-    const long long i0 = s0 + j;
-    if (i0 + VEC <= lo || i0 >= hi) continue;
-    if (i0 >= lo && i0 + VEC <= hi) {
-      uint4 raw = *reinterpret_cast<const uint4*>(in + i0);
-      T x[VEC];
-      *reinterpret_cast<uint4*>(x) = raw;
-      uint32_t bits = ~0u;  // of i0, i0 + 1, ...
-      if (mask) {
-        const int w = (int)(i0 >> 5), s = (int)(i0 & 31);
-        const uint32_t w0 = __ldg(mask + w);
-        const uint32_t w1 = s + VEC > 32 ? __ldg(mask + w + 1) : 0u;
-        bits = __funnelshift_r(w0, w1, s);
-      }
 #pragma unroll
-      for (int q = 0; q < VEC; q += 4) {
-        int4 c = make_int4(0, 0, 0, 0), b = c;
-        if (counts) c = *reinterpret_cast<const int4*>(cnt + j + q);
-        if (biases) b = *reinterpret_cast<const int4*>(badd + j + q);
-        x[q] = from_f<T>(rule(to_f(x[q]), c.x, __int_as_float(b.x), (bits >> q) & 1));
-        x[q + 1] = from_f<T>(rule(to_f(x[q + 1]), c.y, __int_as_float(b.y), (bits >> (q + 1)) & 1));
-        x[q + 2] = from_f<T>(rule(to_f(x[q + 2]), c.z, __int_as_float(b.z), (bits >> (q + 2)) & 1));
-        x[q + 3] = from_f<T>(rule(to_f(x[q + 3]), c.w, __int_as_float(b.w), (bits >> (q + 3)) & 1));
+  for (int u = 0; u < KV; ++u) {
+    const int j = (u * kRuleThreads + tid) * VEC;
+    const long long i0 = s0 + j;
+    if (j < a.run && i0 >= lo && i0 + VEC <= hi) {
+      T x[VEC];
+      *reinterpret_cast<uint4*>(x) = raw[u];
+      if (noted) {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 4) {
+          const int4 w = *reinterpret_cast<const int4*>(note + j + q);
+          if (w.x | w.y | w.z | w.w) {
+            x[q] = from_f<T>(rule(to_f(x[q]), w.x));
+            x[q + 1] = from_f<T>(rule(to_f(x[q + 1]), w.y));
+            x[q + 2] = from_f<T>(rule(to_f(x[q + 2]), w.z));
+            x[q + 3] = from_f<T>(rule(to_f(x[q + 3]), w.w));
+          }
+        }
+      }
+      if (mask) {
+        const int k = (int)(i0 >> 5), sh = (int)(i0 & 31);
+        const uint32_t w0 = __ldg(mask + k);
+        const uint32_t w1 = sh + VEC > 32 ? __ldg(mask + k + 1) : 0u;
+        const uint32_t bits = __funnelshift_r(w0, w1, sh);  // of i0, i0 + 1, ...
+#pragma unroll
+        for (int q = 0; q < VEC; ++q)
+          if (!((bits >> q) & 1)) x[q] = from_f<T>(-INFINITY);
       }
       if (vec_out) {
         *reinterpret_cast<uint4*>(out + i0) = *reinterpret_cast<const uint4*>(x);
@@ -399,21 +420,29 @@ __global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const RuleArg
 #pragma unroll
         for (int q = 0; q < VEC; ++q) out[i0 + q] = x[q];
       }
-    } else {
-      for (int q = 0; q < VEC; ++q) {
-        const long long i = i0 + q;
-        if (i < lo || i >= hi) continue;
-        const bool ok = !mask || ((__ldg(mask + (i >> 5)) >> (i & 31)) & 1);
-        out[i] = from_f<T>(rule(to_f(in[i]), counts ? cnt[j + q] : 0,
-                                biases ? __int_as_float(badd[j + q]) : 0.0f, ok));
-      }
     }
+  }
+  // the run's first and last few, where a 16-byte piece reaches past it
+  const int head = (int)min((long long)hi, s0 + (lo - s0 + VEC - 1) / VEC * VEC);
+  const int tail = (int)max((long long)head, s0 + (hi - s0) / VEC * VEC);
+  for (int i = tid; i < (head - lo) + (hi - tail); i += kRuleThreads) {
+    const int at = i < head - lo ? lo + i : tail + (i - (head - lo));
+    const bool ok = !mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1);
+    const float x = rule(to_f(in[at]), noted ? note[(int)(at - s0)] : 0);
+    out[at] = from_f<T>(ok ? x : -INFINITY);
   }
 }
 
 template <typename T>
 cudaError_t launch_rules(const RuleArgs& a, int n_rows, cudaStream_t st) {
-  const size_t smem = sizeof(int) * a.run * ((a.history ? 1 : 0) + (a.n_bias > 0 ? 1 : 0));
+  const size_t smem =
+      a.history || a.n_bias ? sizeof(int) * ((size_t)a.run + a.n_bias) : 0;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(logit_rules_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(int) * (kRuleRun + kRuleMaxBias));
+    if (e != cudaSuccess) return e;
+  }
   logit_rules_kernel<T><<<(unsigned)(n_rows * a.runs), kRuleThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -525,8 +554,9 @@ extern "C" int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logi
   if (dtype != M3_LOGITS_F32 && dtype != M3_LOGITS_BF16 && dtype != M3_LOGITS_F16)
     return set_error(M3_EINVAL, "dtype");
   if (n_rows < 0 || vocab < 1 || vocab > (1 << 30)) return set_error(M3_EINVAL, "n_rows or vocab");
-  if (n_history < 0 || n_bias < 0 || n_bias > kRuleMaxBias || n_masks < 0)
-    return set_error(M3_EINVAL, "n_history, n_bias (up to 4096) or n_masks");
+  if (n_history < 0 || n_history > kRuleMaxHistory || n_bias < 0 || n_bias > kRuleMaxBias ||
+      n_masks < 0)
+    return set_error(M3_EINVAL, "n_history (up to 524287), n_bias (up to 4095) or n_masks");
   if (n_rows == 0) return M3_OK;
   if (!logits || !out) return set_error(M3_EINVAL, "null argument");
   if (n_bias && (!bias_ids || !bias)) return set_error(M3_EINVAL, "null bias_ids or bias");
@@ -564,9 +594,10 @@ extern "C" int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logi
   a.n_bias = n_bias;
   a.n_masks = n_masks;
   a.words = (vocab + 31) / 32;
-  // a run: 4096 logits, or 1024 where those would leave SMs without a CTA
-  const long long big = ((long long)vocab + 7 + 4095) / 4096;
-  a.run = big * n_rows < 2ll * sm_count() ? 1024 : 4096;
+  // a run: the longest that still gives every SM a CTA, 1024 logits at least
+  a.run = kRuleRun;
+  while (a.run > 1024 && (((long long)vocab + 7 + a.run - 1) / a.run) * n_rows < sm_count())
+    a.run >>= 1;
   a.runs = (int)(((long long)vocab + 7 + a.run - 1) / a.run);
   if ((long long)a.runs * n_rows > INT_MAX) return set_error(M3_EINVAL, "too many rows");
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);

@@ -28,6 +28,18 @@ __device__ int g_ops_err;  // first error word of this file's kernels (m3_ops_sy
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {  // two fp32 lanes
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {  // 2^x, one MUFU instruction; 2^-inf = 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -39,8 +51,8 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, one MUFU instruction; 2
 // head sit side by side in one tile, so a K/V tile is read once for all of
 // them and a causal tile of 128 rows spans few tokens.
 //
-// One CTA, 12 warps: warp 0 brings Q and the K/V tiles by TMA, warp 1 issues
-// the MMAs, warps 4..7 and 8..11 are the softmax of row tiles 0 and 1 with
+// One CTA, 12 warps: warp 0 brings Q and the K/V tiles by TMA, warps 1 and 2
+// issue the MMAs of row tiles 0 and 1, warps 4..7 and 8..11 are the softmax of row tiles 0 and 1 with
 // one row per thread (a TMEM lane is a row: no shuffles).  S = Q K^T goes to
 // tensor memory; the softmax reads it, writes P (16 bit) over it and the next
 // MMA takes P from there, O += P V, also in tensor memory.  The two row
@@ -109,6 +121,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// One lane of a converged warp (the same one each time).  Unlike lane == 0 it
+// lets the compiler keep descriptors in uniform registers: an MMA then issues
+// in fewer cycles than it runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -193,6 +215,7 @@ struct TcWork {
   int hi;         // keys past key0 that exist for these rows
   int pos0;       // packed: the first tile's first token sits at key pos0
   int split;
+  int fix;        // the key tile that reaches past them, or -1
 };
 
 // Packed: the CTA's 2 x tpt tokens.  Sequences are walked 32 at a time.
@@ -262,12 +285,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* empty = full + NS;
   uint64_t* qfull = empty + NS;
   uint64_t* sfull = qfull + 1;   // [2] S of a row tile is there
-  uint64_t* pfull = sfull + 2;   // [2] P is written
-  uint64_t* ofull = pfull + 2;   // [2] the last product is done
-  uint64_t* drain = ofull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  int* counts = reinterpret_cast<int*>(tmem_slot + 1);         // tiles asked for, tiles seen
-  uint32_t* seen_mask = reinterpret_cast<uint32_t*>(counts + 2);  // [8] 16-key pieces of a key tile
+  uint64_t* pfull = sfull + 2;   // [2][2] P is written: keys 0..63, 64..127
+  uint64_t* ofull = pfull + 4;   // [2] the last product is done
+  uint64_t* vfix = ofull + 2;    // the rows past the last key are cleared
+  uint64_t* drain = vfix + 1;    // [2]
+  uint64_t* turn = drain + 2;    // [2] whose products are next
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
+  int* counts = reinterpret_cast<int*>(tmem_slot + 1);  // tiles asked for, seen by each MMA warp
+  uint32_t* seen_mask = reinterpret_cast<uint32_t*>(counts + 3);  // [8] 16-key pieces of a key tile
   __shared__ TcWork work;
   __shared__ int have_work;
 
@@ -301,19 +326,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (lane == 0) {
       have_work = some;
-      if (some) work = k;
+      if (some) {
+        const int n = max(k.n[0], k.n[1]);
+        k.fix = k.hi < n * kTile ? n - 1 : -1;
+        work = k;
+      }
       for (int s = 0; s < NS; ++s) {
         mbar_init(&full[s], 1);
-        mbar_init(&empty[s], 1);
+        mbar_init(&empty[s], 2);
       }
       mbar_init(qfull, 1);
+      mbar_init(vfix, 1);
       for (int t = 0; t < 2; ++t) {
         mbar_init(&sfull[t], 1);
-        mbar_init(&pfull[t], 4);
+        mbar_init(&drain[t], 1);
+        mbar_init(&turn[t], 1);
+        mbar_init(&pfull[2 * t], 4);
+        mbar_init(&pfull[2 * t + 1], 4);
         mbar_init(&ofull[t], 1);
       }
-      mbar_init(drain, 1);
-      counts[0] = counts[1] = 0;
+      counts[0] = counts[1] = counts[2] = 0;
       fence_barrier_init();
     }
   }
@@ -330,14 +362,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  const TcWork w = work;
+  const TcWork& w = work;  // in shared memory: indexed by the row tile
   const int n_max = max(w.n[0], w.n[1]);
   // columns: S (and P over it) of the row tiles at 0 and 128, O at 256 and 384
   const uint32_t idesc_s = tc_idesc<F16, kTile, 0>(), idesc_o = tc_idesc<F16, D, 1>();
 
-  if (warp == 0) {
+  // the softmax holds a row of S in registers: it takes them from the other
+  // four warps (128 x 72 + 256 x 216 = 384 x 168, the launch's own total)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ------------------------------------------------------------- TMA --
-    if (lane == 0 && n_max > 0) {
+    if (warp == 0 && lane == 0 && n_max > 0) {
       const uint32_t qbytes = (uint32_t)(a.grp * a.tpt) * D * 2;
       mbar_arrive_expect_tx(qfull, ((w.n[0] > 0) + (w.n[1] > 0)) * qbytes);
       for (int t = 0; t < 2; ++t)
@@ -384,125 +419,152 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       counts[0] = it;
     }
-  } else if (warp == 1) {
+    if (warp == 0 && w.fix >= 0) {
+      // what lies past the keys in the last tile may be anything, and 0 * NaN
+      // is not 0: those rows of V are cleared.  (By this warp, which has seen
+      // the slot's earlier uses end: another could take an earlier phase of
+      // the barrier for this one.)
+      __syncwarp();
+      const int i = 2 * w.fix + 1, rows = w.hi - w.fix * kTile;
+      if (mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u, err)) {
+        uint8_t* v = skv + (size_t)(i % NS) * S::tile_bytes;
+        for (int p = rows * 8 + lane; p < kTile * 8; p += 32)
+          for (int c = 0; c < D / 64; ++c)
+            *reinterpret_cast<uint4*>(v + c * S::half_bytes + p * 16) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vfix);
+    }
     // ------------------------------------------------------------- MMA --
-    int seen = 0;
-    bool ok = true;
-    auto wait_tile = [&](int i) {
-      ok = ok && mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u, err);
-      if (ok) seen = i + 1;
-    };
-    auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
-      if (lane == 0) {
-        const uint32_t qa = smem_u32(sq + t * S::tile_bytes);
-        const uint32_t kb = smem_u32(skv + (size_t)((2 * j) % NS) * S::tile_bytes);
+    // A warp per row tile: the waits of one tile hide behind the products of
+    // the other.  Both see every K/V tile, since both have to give it back.
+    // They take turns, O += P V and the next S = Q K^T of one tile together:
+    // left alone the tiles fall into step, and then both softmaxes compete for
+    // the exponentials while the tensor cores wait.
+    if ((warp == 1 || warp == 2) && n_max > 0) {
+      const int t = warp - 1, mine = w.n[t];
+      const uint32_t ts = tmem + t * kTile, to = tmem + 256 + t * kTile;
+      const uint64_t dq = kdesc(smem_u32(sq + t * S::tile_bytes)), dk = kdesc(smem_u32(skv));
+      const uint64_t dv = vdesc(smem_u32(skv), S::half_bytes);
+      int slot = 0, seen = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto wait_tile = [&]() {  // the next tile of the ring
+        ok = ok && mbar_wait(&full[slot], phase, err);
+        seen += ok;
+      };
+      auto give_back = [&]() {  // once this thread's MMAs so far are done
+        mma_commit(&empty[slot]);
+      };
+      auto next_slot = [&]() {
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
+      auto scores = [&]() {  // S = Q K^T
+        const uint64_t b0 = dk + (uint64_t)slot * (S::tile_bytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * S::half_bytes + (ks % 4) * 32;
-          mma_ss(tmem + t * kTile, kdesc(qa + off), kdesc(kb + off), idesc_s, ks > 0);
+          const uint32_t off = ((ks / 4) * S::half_bytes + (ks % 4) * 32) >> 4;
+          mma_ss(ts, dq + off, b0 + off, idesc_s, ks > 0);
         }
         mma_commit(&sfull[t]);
-      }
-    };
-    if (n_max > 0) {
+      };
       ok = mbar_wait(qfull, 0, err);
-      wait_tile(0);
+      wait_tile();
       fence_after();
-      if (ok) {
-        for (int t = 0; t < 2; ++t)
-          if (w.n[t] > 0) scores(t, 0);
-        if (lane == 0) mma_commit(&empty[0]);
+      if (ok && elect_one()) {
+        if (mine > 0) scores();
+        give_back();
       }
+      __syncwarp();
+      next_slot();
       for (int j = 0; j < n_max && ok; ++j) {
-        wait_tile(2 * j + 1);
-        if (!ok) break;
-        const uint32_t vb = smem_u32(skv + (size_t)((2 * j + 1) % NS) * S::tile_bytes);
-        const int rows = w.hi - j * kTile;
-        if (rows < kTile) {
-          // the last tile: what lies past the keys may be anything, and
-          // 0 * NaN is not 0
-          uint8_t* v = skv + (size_t)((2 * j + 1) % NS) * S::tile_bytes;
-          for (int i = rows * 8 + lane; i < kTile * 8; i += 32)
-            for (int c = 0; c < D / 64; ++c)
-              *reinterpret_cast<uint4*>(v + c * S::half_bytes + i * 16) = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        wait_tile();
+        if (ok && j == w.fix) ok = mbar_wait(vfix, 0, err);
+        const uint64_t b0 = dv + (uint64_t)slot * (S::tile_bytes >> 4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (j < mine) ok = ok && mbar_wait(&pfull[2 * t + half], (uint32_t)j & 1u, err);
+          // (a warp without work waits too: it must not run two turns ahead)
+          if (!half && (t || j)) ok = ok && mbar_wait(&turn[t], (uint32_t)(j + t + 1) & 1u, err);
+          if (j >= mine) break;
+          fence_after();
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int k4 = 0; k4 < kTile / 32; ++k4) {  // 16 keys a step: 2048 bytes of V rows
+              const int ks = half * (kTile / 32) + k4;
+              mma_ts(to, ts + ks * 8, b0 + ks * (2048 >> 4), idesc_o, (j > 0 || ks > 0));
+            }
+            if (half) {
+              give_back();
+              if (j + 1 == mine) mma_commit(&ofull[t]);
+            }
+          }
           __syncwarp();
         }
-        bool next = false;  // K of the next tile is there
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j >= w.n[t]) continue;
-          ok = mbar_wait(&pfull[t], (uint32_t)j & 1u, err);
-          if (!ok) break;
-          fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)  // 16 keys a step: 2048 bytes of V rows
-              mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + ks * 8,
-                     vdesc(vb + ks * 2048, S::half_bytes), idesc_o, (j > 0 || ks > 0));
-          }
-          if (j + 1 < w.n[t]) {
-            if (!next) {
-              wait_tile(2 * j + 2);
-              if (!ok) break;
-              fence_after();
-              next = true;
-            }
-            scores(t, j + 1);
-          } else if (lane == 0) {
-            mma_commit(&ofull[t]);
-          }
-        }
-        if (ok && lane == 0) {
-          mma_commit(&empty[(2 * j + 1) % NS]);
-          if (j + 1 < n_max) mma_commit(&empty[(2 * j + 2) % NS]);
-        }
+        if (ok && j >= mine && elect_one()) give_back();
         __syncwarp();
+        next_slot();
+        if (!ok) break;
+        if (j + 1 < n_max) {
+          wait_tile();
+          fence_after();
+          if (ok && elect_one()) {
+            if (j + 1 < mine) scores();
+            give_back();
+          }
+          __syncwarp();
+          next_slot();
+        }
+        if (lane == 0) mbar_arrive(&turn[1 - t]);
       }
-      if (!ok && lane == 0) {  // this thread's MMAs finish before the memory goes away
-        mma_commit(drain);
-        for (long long i = 0; i < kSpinLimit && !mbar_try_wait(drain, 0); ++i) {
+      if (!ok && elect_one()) {  // this thread's MMAs finish before the memory goes away
+        mma_commit(&drain[t]);
+        for (long long i = 0; i < kSpinLimit && !mbar_try_wait(&drain[t], 0); ++i) {
         }
       }
+      if (lane == 0) counts[1 + t] = seen;
     }
-    if (lane == 0) counts[1] = seen;
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // --------------------------------------------------------- softmax --
     const int t = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t base = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t ts = base + t * kTile, to = base + 256 + t * kTile;
-    const int tok = row / a.grp, head = w.h * a.grp + row % a.grp;
+    const int tok = row / a.grp, head = w.h * a.grp + row % a.grp, tiles = w.n[t];
     const bool mine = tok < w.count[t] && row < a.grp * a.tpt;
     // keys this row attends to, counted from key0
     const int keys = PAGED ? w.hi : w.pos0 + t * a.tpt + tok + 1;
     float m = -INFINITY, l = 0.0f;  // reference maximum (of q.k), sum of 2^((s - m) c)
     bool ok = true;
-    for (int j = 0; j < w.n[t]; ++j) {
+    for (int j = 0; j < tiles; ++j) {
       ok = mbar_wait(&sfull[t], (uint32_t)j & 1u, err);
       if (!ok) break;
       fence_after();
       uint32_t s[kTile];
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const int lim = keys - j * kTile;
+      uint32_t there = 0xFFu;
+      if constexpr (PAGED) there = *reinterpret_cast<volatile uint32_t*>(&seen_mask[j & 7]);
+      const bool cut = lim < kTile || there != 0xFFu;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tm_ld(ts + 32 * i, s + 32 * i);
+      for (int k = 0; k < 4; ++k) tm_ld(ts + 32 * k, s + 32 * k);
       ld_wait();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ld_touch(s + 32 * i);
-      const int lim = keys - j * kTile;
-      if (lim < kTile) {
+      for (int k = 0; k < 4; ++k) ld_touch(s + 32 * k);
+      if (cut) {
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) s[i] = i < lim ? s[i] : 0xFF800000u;
+        for (int i = 0; i < kTile; ++i)
+          s[i] = i < lim && ((there >> (i / 16)) & 1) ? s[i] : 0xFF800000u;
       }
-      if constexpr (PAGED) {
-        const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&seen_mask[j & 7]);
-        if (there != 0xFFu) {
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] = (there >> (i / 16)) & 1 ? s[i] : 0xFF800000u;
-        }
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      for (int i = 0; i < kTile; i += 8)
 #pragma unroll
-      for (int i = 0; i < kTile; i += 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[i + e]));
+        for (int e = 0; e < 4; ++e)
+          mx[e] = max3(mx[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool raise = (top - m) * a.c > kRaise || (m == -INFINITY && top > m);
       if (__any_sync(~0u, raise)) {
@@ -524,33 +586,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       const float mc = m == -INFINITY ? 0.0f : m * a.c;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const uint64_t c2 = pack_f32x2(a.c, a.c), mc2 = pack_f32x2(-mc, -mc);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < kTile; i += 64) {
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float x = ex2(fmaf(__uint_as_float(s[i + 2 * e]), a.c, -mc));
-          const float y = ex2(fmaf(__uint_as_float(s[i + 2 * e + 1]), a.c, -mc));
-          sum[e & 1] += x;
-          sum[2 + (e & 1)] += y;
+          const float2 z = unpack_f32x2(fma2(pack_u32x2(s[i + 2 * e], s[i + 2 * e + 1]), c2, mc2));
+          const float x = ex2(z.x), y = ex2(z.y);
+          fadd2(sum[e & 1], pack_f32x2(x, y));
           p[e] = pack2<F16>(x, y);  // the weights in the operand type of the product with V
         }
         tm_st(ts + i / 2, p);
+        // half of the keys: their product may start
+        st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * t + i / 64]);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[t]);
+      fadd2(sum[0], sum[1]);
+      const float2 sums = unpack_f32x2(sum[0]);
+      l += sums.x + sums.y;
     }
     // ----------------------------------------------------------- output --
-    if (w.n[t] > 0 && ok) {
+    if (tiles > 0 && ok) {
       ok = mbar_wait(&ofull[t], 0, err);
       fence_after();
     }
     if (ok) {
-      const bool some = w.n[t] > 0;
+      const bool some = tiles > 0;
       const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
       if constexpr (PAGED) {
         const size_t id = (size_t)w.split * a.n_rows * a.Hq + (size_t)(w.first[t] + tok) * a.Hq + head;
@@ -605,7 +670,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // copies asked for but never seen (only after a failed wait): let them land
     for (long long k = 0; k < kSpinLimit && !mbar_try_wait(qfull, 0); ++k) {
     }
-    for (int i = counts[1]; i < counts[0]; ++i)
+    for (int i = min(counts[1], counts[2]); i < counts[0]; ++i)
       for (long long k = 0; k < kSpinLimit && !mbar_try_wait(&full[i % NS], (uint32_t)(i / NS) & 1u);
            ++k) {
       }
