@@ -243,17 +243,32 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs
 }
 
 // ----------------------------------------------------------------- rules ---
-// A CTA takes a run of one row's vocabulary.  It asks for its logits first;
-// while they come it notes in one word of shared memory per token how often
-// the row's history has it (whole numbers: the order of the atomics does not
-// matter) and which bias entry is its own; then the rules, from registers, and
-// one write.  Few tokens have a word other than 0, so most pieces only meet
-// the mask.  Every run of a row reads the whole history again, so runs are
-// long.
+// A CTA takes a run of one row's vocabulary.  It asks for everything it will
+// need at once -- its logits, the mask's words, the history, the biases -- then
+// notes in one word of shared memory per token how often the row's history has
+// it and whether a bias names it (additions and a flag: the order of the
+// atomics does not matter).  Meanwhile the logits are written out under the
+// mask alone: few tokens have a word other than 0, and those are taken up again
+// afterwards, from a list, where the mask has left them as they were.  (Rules
+// inside the streaming loop bind the kernel by its instructions.)  Every run of a row reads the whole history again, so runs
+// are long.
 constexpr int kRuleThreads = 512;
 constexpr int kRuleRun = 8192;  // logits of the longest run
-constexpr int kCountBits = 19;  // of the word: the count; above it the bias entry's code
-constexpr int kRuleMaxBias = 4095, kRuleMaxHistory = (1 << kCountBits) - 1;
+constexpr int kBiased = 1 << 30;  // of the word: a bias names the token; below it the count
+constexpr int kRuleMaxBias = 4096, kRuleMaxHistory = 1 << 24;  // counts are exact in fp32
+
+// atom.shared as it stands: the compiler's own form for a counter gathers the
+// warp's lanes first, some 20 instructions at each place it is used.
+__device__ __forceinline__ int smem_add(int* p, int v) {
+  int old;
+  asm volatile("atom.shared.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(p)), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ int smem_or(int* p, int v) {
+  int old;
+  asm volatile("atom.shared.or.b32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(p)), "r"(v) : "memory");
+  return old;
+}
 
 struct RuleArgs {
   const void* in;
@@ -280,7 +295,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 
 template <typename T>
-__global__ void __launch_bounds__(kRuleThreads, 2) logit_rules_kernel(const RuleArgs a) {
+__global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const RuleArgs a) {
   constexpr int VEC = 16 / sizeof(T);
   constexpr int KV = kRuleRun / (VEC * kRuleThreads);  // 16-byte pieces per thread
   extern __shared__ int rule_smem[];
@@ -308,84 +323,84 @@ __global__ void __launch_bounds__(kRuleThreads, 2) logit_rules_kernel(const Rule
     const int m = a.mask_row ? __ldg(a.mask_row + row) : (a.n_masks == 1 ? 0 : row);
     if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * a.words;
   }
+  uint32_t mbits[KV];
+#pragma unroll
+  for (int u = 0; u < KV; ++u) {
+    const long long i0 = s0 + (u * kRuleThreads + tid) * VEC;
+    mbits[u] = mask && i0 >= lo && i0 < hi ? __ldg(mask + (i0 >> 5)) : 0u;
+  }
   const bool counts = a.history != nullptr, biases = a.n_bias > 0, noted = counts || biases;
-  int* note = rule_smem;                                       // [run]
-  float* bsum = reinterpret_cast<float*>(rule_smem + a.run);  // [n_bias] of the entries that own a token
+  const int32_t* hist = a.history + (counts ? row * a.ld_history : 0);
+  const bool hvec = counts && (reinterpret_cast<uintptr_t>(hist) & 15) == 0;
+  int n_hist = a.n_history;
+  int4 h0 = make_int4(-1, -1, -1, -1), h1 = h0;  // the first of the history
+  if (hvec) {
+    if (tid < n_hist >> 2) h0 = __ldg(reinterpret_cast<const int4*>(hist) + tid);
+    if (tid + kRuleThreads < n_hist >> 2)
+      h1 = __ldg(reinterpret_cast<const int4*>(hist) + tid + kRuleThreads);
+  }
+  if (counts && a.hist_len) n_hist = min(n_hist, max(0, __ldg(a.hist_len + row)));
+  const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
+  const float* val = a.bias + (size_t)row * a.n_bias;
+  int id0 = -1;
+  float val0 = 0.0f;
+  if (tid < a.n_bias) {
+    id0 = __ldg(ids + tid);
+    val0 = __ldg(val + tid);
+  }
+  int* note = rule_smem;                                    // [run]
+  int4* named = reinterpret_cast<int4*>(rule_smem + a.run);  // [n_bias] (token, entry, bias)
+  uint16_t* list = reinterpret_cast<uint16_t*>(named + a.n_bias);  // [run] tokens noted, from s0
+  __shared__ int n_named, n_list;
   if (noted) {
+    if (tid == 0) n_named = n_list = 0;
     for (int i = tid * 4; i < a.run; i += kRuleThreads * 4)
       *reinterpret_cast<int4*>(note + i) = make_int4(0, 0, 0, 0);
     __syncthreads();
   }
-  if (biases) {
-    // the first entry of each token owns it: entry e has the code n_bias - e
-    // and the largest stays, whatever the order; the owner adds up the token's
-    // entries in their order, looking past itself only where a token came twice
-    __shared__ int twice;
-    const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
-    const float* val = a.bias + (size_t)row * a.n_bias;
-    if (tid == 0) twice = 0;
-    for (int e = tid; e < a.n_bias; e += kRuleThreads) {
-      const int id = __ldg(ids + e);
-      if (id >= lo && id < hi) {
-        bsum[e] = __ldg(val + e);
-        atomicMax(&note[(int)(id - s0)], (a.n_bias - e) << kCountBits);
-      }
-    }
-    __syncthreads();
-    bool again = false;
-    for (int e = tid; e < a.n_bias; e += kRuleThreads) {
-      const int id = __ldg(ids + e);
-      if (id >= lo && id < hi && note[(int)(id - s0)] >> kCountBits != a.n_bias - e) again = true;
-    }
-    if (again) twice = 1;
-    __syncthreads();
-    if (twice) {
-      for (int e = tid; e < a.n_bias; e += kRuleThreads) {
-        const int id = __ldg(ids + e);
-        if (id >= lo && id < hi && note[(int)(id - s0)] >> kCountBits == a.n_bias - e)
-          for (int f = e + 1; f < a.n_bias; ++f)
-            if (__ldg(ids + f) == id) bsum[e] += __ldg(val + f);
-      }
-    }
-  }
   if (counts) {
-    const int32_t* h = a.history + row * a.ld_history;
-    int n = a.n_history;
-    if (a.hist_len) n = min(n, max(0, __ldg(a.hist_len + row)));
+    const unsigned span = (unsigned)(hi - lo);
     auto add = [&](int id) {
-      if (id >= lo && id < hi) atomicAdd(&note[(int)(id - s0)], 1);
+      if ((unsigned)id - (unsigned)lo >= span) return;
+      const int at = (int)(id - s0);
+      if (smem_add(&note[at], 1) == 0) list[smem_add(&n_list, 1)] = (uint16_t)at;
     };
-    if ((reinterpret_cast<uintptr_t>(h) & 15) == 0) {
-      const int n4 = n >> 2;
-#pragma unroll 2
-      for (int i = tid; i < n4; i += kRuleThreads) {
-        const int4 v = __ldg(reinterpret_cast<const int4*>(h) + i);
-        add(v.x);
-        add(v.y);
-        add(v.z);
-        add(v.w);
+    auto add4 = [&](int i, int4 v) {
+      if (4 * i + 4 > n_hist) {  // the last piece: places past the end name no token
+        v.x = 4 * i < n_hist ? v.x : -1;
+        v.y = 4 * i + 1 < n_hist ? v.y : -1;
+        v.z = 4 * i + 2 < n_hist ? v.z : -1;
+        v.w = -1;
       }
-      for (int i = (n4 << 2) + tid; i < n; i += kRuleThreads) add(__ldg(h + i));
-    } else {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kRuleThreads) add(__ldg(h + i));
+      add(v.x);
+      add(v.y);
+      add(v.z);
+      add(v.w);
+    };
+    int done = 0;
+    if (hvec) {
+      add4(tid, h0);
+      add4(tid + kRuleThreads, h1);
+      const int had = min(8 * kRuleThreads, a.n_history & ~3);  // places h0 and h1 cover
+      for (int i = had / 4 + tid; i < n_hist >> 2; i += kRuleThreads)
+        add4(i, __ldg(reinterpret_cast<const int4*>(hist) + i));
+      done = max(had, n_hist & ~3);
     }
+    for (int i = done + tid; i < n_hist; i += kRuleThreads) add(__ldg(hist + i));
   }
-  if (noted) __syncthreads();
+  if (biases) {
+    auto name = [&](int e, int id, float b) {
+      if (id < lo || id >= hi) return;
+      if (smem_or(&note[(int)(id - s0)], kBiased) == 0)
+        list[smem_add(&n_list, 1)] = (uint16_t)(id - s0);
+      named[smem_add(&n_named, 1)] = make_int4(id, e, __float_as_int(b), 0);
+    };
+    name(tid, id0, val0);
+    for (int e = tid + kRuleThreads; e < a.n_bias; e += kRuleThreads)
+      name(e, __ldg(ids + e), __ldg(val + e));
+  }
 
-  // x / repetition as a product with its reciprocal: one more rounding in
-  // fp32, no division per logit
-  const float inv = 1.0f / rep;
-  auto rule = [&](float x, int w) -> float {
-    const int c = w & ((1 << kCountBits) - 1), code = w >> kCountBits;
-    if (c > 0) {
-      x = x > 0.0f ? x * inv : x * rep;
-      x -= freq * (float)c;
-      x -= pres;
-    }
-    if (code > 0) x += bsum[a.n_bias - code];
-    return x;
-  };
+  // the run under the mask alone
 #pragma unroll
   for (int u = 0; u < KV; ++u) {
     const int j = (u * kRuleThreads + tid) * VEC;
@@ -393,23 +408,10 @@ __global__ void __launch_bounds__(kRuleThreads, 2) logit_rules_kernel(const Rule
     if (j < a.run && i0 >= lo && i0 + VEC <= hi) {
       T x[VEC];
       *reinterpret_cast<uint4*>(x) = raw[u];
-      if (noted) {
-#pragma unroll
-        for (int q = 0; q < VEC; q += 4) {
-          const int4 w = *reinterpret_cast<const int4*>(note + j + q);
-          if (w.x | w.y | w.z | w.w) {
-            x[q] = from_f<T>(rule(to_f(x[q]), w.x));
-            x[q + 1] = from_f<T>(rule(to_f(x[q + 1]), w.y));
-            x[q + 2] = from_f<T>(rule(to_f(x[q + 2]), w.z));
-            x[q + 3] = from_f<T>(rule(to_f(x[q + 3]), w.w));
-          }
-        }
-      }
       if (mask) {
-        const int k = (int)(i0 >> 5), sh = (int)(i0 & 31);
-        const uint32_t w0 = __ldg(mask + k);
-        const uint32_t w1 = sh + VEC > 32 ? __ldg(mask + k + 1) : 0u;
-        const uint32_t bits = __funnelshift_r(w0, w1, sh);  // of i0, i0 + 1, ...
+        const int sh = (int)(i0 & 31);
+        const uint32_t w1 = sh + VEC > 32 ? __ldg(mask + (i0 >> 5) + 1) : 0u;
+        const uint32_t bits = __funnelshift_r(mbits[u], w1, sh);  // of i0, i0 + 1, ...
 #pragma unroll
         for (int q = 0; q < VEC; ++q)
           if (!((bits >> q) & 1)) x[q] = from_f<T>(-INFINITY);
@@ -422,25 +424,61 @@ __global__ void __launch_bounds__(kRuleThreads, 2) logit_rules_kernel(const Rule
       }
     }
   }
-  // the run's first and last few, where a 16-byte piece reaches past it
+  auto allowed = [&](int at) { return !mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1); };
+  // its first and last few, where a 16-byte piece reaches past it
   const int head = (int)min((long long)hi, s0 + (lo - s0 + VEC - 1) / VEC * VEC);
   const int tail = (int)max((long long)head, s0 + (hi - s0) / VEC * VEC);
-  for (int i = tid; i < (head - lo) + (hi - tail); i += kRuleThreads) {
-    const int at = i < head - lo ? lo + i : tail + (i - (head - lo));
-    const bool ok = !mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1);
-    const float x = rule(to_f(in[at]), noted ? note[(int)(at - s0)] : 0);
-    out[at] = from_f<T>(ok ? x : -INFINITY);
+  if (tid < (head - lo) + (hi - tail)) {
+    const int at = tid < head - lo ? lo + tid : tail + (tid - (head - lo));
+    out[at] = allowed(at) ? in[at] : from_f<T>(-INFINITY);
+  }
+  if (!noted) return;
+  __syncthreads();  // the notes are complete, and what this CTA wrote is there
+
+  // x / repetition as a product with its reciprocal: one more rounding in
+  // fp32, no division
+  const float inv = 1.0f / rep;
+  for (int k = tid; k < n_list; k += kRuleThreads) {
+    const int w = note[list[k]], at = (int)(s0 + list[k]);
+    if (!allowed(at)) continue;
+    float x = to_f(in[at]);  // from L1; out's, where that is logits, is the same
+    const int c = w & (kBiased - 1);
+    if (c > 0) {
+      x = x > 0.0f ? x * inv : x * rep;
+      x -= freq * (float)c;
+      x -= pres;
+    }
+    if (w & kBiased) {
+      // the run's few biases stand in no order: the token's are added in theirs
+      float b = 0.0f;
+      for (int last = -1;;) {
+        int e = INT_MAX;
+        float v = 0.0f;
+        for (int i = 0; i < n_named; ++i) {
+          const int4 n = named[i];
+          if (n.x == at && n.y > last && n.y < e) {
+            e = n.y;
+            v = __int_as_float(n.z);
+          }
+        }
+        if (e == INT_MAX) break;
+        b += v;
+        last = e;
+      }
+      x += b;
+    }
+    out[at] = from_f<T>(x);
   }
 }
 
 template <typename T>
 cudaError_t launch_rules(const RuleArgs& a, int n_rows, cudaStream_t st) {
   const size_t smem =
-      a.history || a.n_bias ? sizeof(int) * ((size_t)a.run + a.n_bias) : 0;
-  if (smem > 48 * 1024) {
+      a.history || a.n_bias ? 6 * (size_t)a.run + 16 * (size_t)a.n_bias : 0;
+  if (smem > 40 * 1024) {  // past the default limit with what the kernel holds itself
     const cudaError_t e =
         cudaFuncSetAttribute(logit_rules_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(int) * (kRuleRun + kRuleMaxBias));
+                             6 * kRuleRun + 16 * kRuleMaxBias);
     if (e != cudaSuccess) return e;
   }
   logit_rules_kernel<T><<<(unsigned)(n_rows * a.runs), kRuleThreads, smem, st>>>(a);
@@ -505,7 +543,7 @@ extern "C" int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
   if (grid > 2 * nsm) grid = 2 * nsm;
   if (grid < 1) grid = 1;
   const size_t smem = sizeof(int) * (2 * (size_t)n_req + 1);
-  if (smem > 48 * 1024)
+  if (smem > 40 * 1024)
     OPS_CK(cudaFuncSetAttribute(kv_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(sizeof(int) * (2 * (size_t)kMapMaxReq + 1))));
   kv_map_kernel<<<(unsigned)grid, kMapThreads, smem, static_cast<cudaStream_t>(cuda_stream)>>>(a);
@@ -556,7 +594,7 @@ extern "C" int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logi
   if (n_rows < 0 || vocab < 1 || vocab > (1 << 30)) return set_error(M3_EINVAL, "n_rows or vocab");
   if (n_history < 0 || n_history > kRuleMaxHistory || n_bias < 0 || n_bias > kRuleMaxBias ||
       n_masks < 0)
-    return set_error(M3_EINVAL, "n_history (up to 524287), n_bias (up to 4095) or n_masks");
+    return set_error(M3_EINVAL, "n_history (up to 2^24), n_bias (up to 4096) or n_masks");
   if (n_rows == 0) return M3_OK;
   if (!logits || !out) return set_error(M3_EINVAL, "null argument");
   if (n_bias && (!bias_ids || !bias)) return set_error(M3_EINVAL, "null bias_ids or bias");

@@ -16,6 +16,7 @@
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "launch.cuh"
 #include "m3_ops.h"
 #include "ops.cuh"
 
@@ -51,9 +52,8 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, one MUFU instruction; 2
 // head sit side by side in one tile, so a K/V tile is read once for all of
 // them and a causal tile of 128 rows spans few tokens.
 //
-// One CTA, 12 warps: warp 0 brings Q and the K/V tiles by TMA, warps 1 and 2
-// issue the MMAs of row tiles 0 and 1, warps 4..7 and 8..11 are the softmax of row tiles 0 and 1 with
-// one row per thread (a TMEM lane is a row: no shuffles).  S = Q K^T goes to
+// One CTA: warp 0 brings Q and the K/V tiles by TMA, warps 1 and 2 issue the
+// MMAs of row tiles 0 and 1, warps 4..7 and 8..11 are their softmax with one row per thread (a TMEM lane is a row: no shuffles).  S = Q K^T goes to
 // tensor memory; the softmax reads it, writes P (16 bit) over it and the next
 // MMA takes P from there, O += P V, also in tensor memory.  The two row
 // tiles alternate: while one's softmax runs, the other's products do.
@@ -61,16 +61,20 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, one MUFU instruction; 2
 // The running maximum is raised, and O rescaled, only when a row's maximum
 // has grown by more than 2^8 since (P then stays below 2^8, and sums and
 // products are relative to the same reference, so nothing is lost).
-constexpr int kTcThreads = 384;
 constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
 constexpr float kRaise = 8.0f;       // log2 units
 
-template <int D>
+// NT row tiles.  Two are for whole SMs of work.  With one the CTA leaves room
+// for another kernel's beside it (m3_attn_prefix: a CTA of attn_own_kernel) and
+// a call of few rows spreads over twice as many SMs.
+template <int D, int NT>
 struct TcShape {
+  static constexpr int threads = 128 + 128 * NT;
+  static constexpr int columns = 256 * NT;                // of tensor memory: S, then O
   static constexpr uint32_t tile_bytes = kTile * D * 2;  // Q, K and V tiles alike
   static constexpr uint32_t half_bytes = kTile * 64 * 2;  // 64 dims of a tile: one swizzled block
-  static constexpr int slots = D == 128 ? 5 : 8;          // K/V ring
-  static constexpr size_t smem = 1024 + (2 + slots) * (size_t)tile_bytes + 512;
+  static constexpr int slots = D == 128 ? (NT == 2 ? 5 : 3) : (NT == 2 ? 8 : 6);  // K/V ring
+  static constexpr size_t smem = 1024 + (NT + slots) * (size_t)tile_bytes + 512;
 };
 
 struct AttnTcArgs {
@@ -218,9 +222,10 @@ struct TcWork {
   int fix;        // the key tile that reaches past them, or -1
 };
 
-// Packed: the CTA's 2 x tpt tokens.  Sequences are walked 32 at a time.
+// Packed: the CTA's NT x tpt tokens.  Sequences are walked 32 at a time.
+template <int NT>
 __device__ __forceinline__ bool find_prompt_work(const AttnTcArgs& a, int w, int lane, TcWork& k) {
-  const int span = 2 * a.tpt;
+  const int span = NT * a.tpt;
   int before = 0;
   for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
     const int s = s0 + lane;
@@ -259,7 +264,7 @@ __device__ __forceinline__ bool find_prompt_work(const AttnTcArgs& a, int w, int
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         k.first[t] = qa + t0 + t * a.tpt;
-        k.count[t] = min(max(lq - t0 - t * a.tpt, 0), a.tpt);
+        k.count[t] = t < NT ? min(max(lq - t0 - t * a.tpt, 0), a.tpt) : 0;
         const int keys = k.count[t] ? max(k.pos0 + t * a.tpt + k.count[t], 0) : 0;
         k.n[t] = (keys + kTile - 1) / kTile;
         k.hi = max(k.hi, keys);
@@ -271,16 +276,16 @@ __device__ __forceinline__ bool find_prompt_work(const AttnTcArgs& a, int w, int
   return false;
 }
 
-template <int D, int F16, bool PAGED>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int D, int F16, bool PAGED, int NT>
+__global__ void __launch_bounds__(384, 1)  // 168 registers, with one row tile (256 threads) too
     attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const AttnTcArgs a) {
-  using S = TcShape<D>;
+  using S = TcShape<D, NT>;
   constexpr int NS = S::slots;
   extern __shared__ uint8_t tc_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)tc_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sq = smem;                         // two row tiles
-  uint8_t* skv = smem + 2 * S::tile_bytes;    // ring: K 0, V 0, K 1, V 1, ...
+  uint8_t* sq = smem;                         // NT row tiles
+  uint8_t* skv = smem + NT * S::tile_bytes;    // ring: K 0, V 0, K 1, V 1, ...
   uint64_t* full = reinterpret_cast<uint64_t*>(skv + NS * (size_t)S::tile_bytes);
   uint64_t* empty = full + NS;
   uint64_t* qfull = empty + NS;
@@ -314,13 +319,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       k.pos0 = 0;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        k.first[t] = (unit * 2 + t) * a.tpt;
-        k.count[t] = min(max(a.n_rows - k.first[t], 0), a.tpt);
+        k.first[t] = (unit * NT + t) * a.tpt;
+        k.count[t] = t < NT ? min(max(a.n_rows - k.first[t], 0), a.tpt) : 0;
         k.n[t] = k.count[t] ? nj : 0;
       }
       some = true;
     } else {
-      some = find_prompt_work(a, blockIdx.x / a.Hkv, lane, k);
+      some = find_prompt_work<NT>(a, blockIdx.x / a.Hkv, lane, k);
       k.h = blockIdx.x % a.Hkv;
       k.split = 0;
     }
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       for (int s = 0; s < NS; ++s) {
         mbar_init(&full[s], 1);
-        mbar_init(&empty[s], 2);
+        mbar_init(&empty[s], NT);
       }
       mbar_init(qfull, 1);
       mbar_init(vfix, 1);
@@ -350,11 +355,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   __syncthreads();
+  // (m3_attn_prefix: the row's own positions need nothing from here)
+  if constexpr (PAGED) pdl_launch_dependents();
   if (!have_work) return;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
-                 "r"(512)
+                 "r"(S::columns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -364,60 +371,77 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const TcWork& w = work;  // in shared memory: indexed by the row tile
   const int n_max = max(w.n[0], w.n[1]);
-  // columns: S (and P over it) of the row tiles at 0 and 128, O at 256 and 384
+  // columns: S (and P over it) of row tile t at 128 t, O at 128 (NT + t)
   const uint32_t idesc_s = tc_idesc<F16, kTile, 0>(), idesc_o = tc_idesc<F16, D, 1>();
 
   // the softmax holds a row of S in registers: it takes them from the other
-  // four warps (128 x 72 + 256 x 216 = 384 x 168, the launch's own total)
+  // four warps (NT = 2: 128 x 72 + 256 x 216 = 384 x 168, the launch's own
+  // total; NT = 1: 128 x 72 + 128 x 216 < 256 x 168)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ------------------------------------------------------------- TMA --
-    if (warp == 0 && lane == 0 && n_max > 0) {
-      const uint32_t qbytes = (uint32_t)(a.grp * a.tpt) * D * 2;
-      mbar_arrive_expect_tx(qfull, ((w.n[0] > 0) + (w.n[1] > 0)) * qbytes);
-      for (int t = 0; t < 2; ++t)
-        if (w.n[t] > 0)
-          for (int c = 0; c < D / 64; ++c)
-            tma_3d(sq + t * S::tile_bytes + c * S::half_bytes, &tq, c * 64, w.h * a.grp, w.first[t],
-                   qfull);
-      bool ok = true;
-      int it = 0;
-      for (int j = 0; j < n_max && ok; ++j) {
-        int number[8];  // pages of this key tile (PAGED), one per box
-        const int page = 1 << a.shift, box = min(page, kTile), boxes = kTile / box;
-        if constexpr (PAGED) {
-          uint32_t m = 0;
-          for (int i = 0; i < boxes; ++i) {
-            const int p = (w.key0 + j * kTile + i * box) >> a.shift;
-            int x = p < a.n_prefix_pages && (long long)p * page < a.prefix_len ? a.pages[p] : -1;
-            if (x < 0 || x >= a.n_pages) x = -1;
-            number[i] = x;
-            if (x >= 0) m |= ((1u << (box / 16)) - 1) << (i * (box / 16));
-          }
-          seen_mask[j & 7] = m;
-        }
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int s = it % NS, use = it / NS;
-          if (use > 0 && !(ok = mbar_wait(&empty[s], (uint32_t)(use - 1) & 1u, err))) break;
-          uint8_t* dst = skv + (size_t)s * S::tile_bytes;
-          mbar_arrive_expect_tx(&full[s], S::tile_bytes);
-          if constexpr (PAGED) {
-            for (int i = 0; i < boxes; ++i) {
-              // a page that is not there: past the pool, which reads as zeros
-              const int x = number[i] < 0 ? a.n_pages : number[i];
-              const int off = (w.key0 + j * kTile + i * box) & (page - 1);
-              for (int c = 0; c < D / 64; ++c)
-                tma_4d(dst + c * S::half_bytes + i * box * 128, &tk, c * 64, off,
-                       w.h + kv * a.Hkv, x, &full[s]);
-            }
-          } else {
+    if (warp == 0 && n_max > 0) {
+      if (lane == 0) {
+        const uint32_t qbytes = (uint32_t)(a.grp * a.tpt) * D * 2;
+        mbar_arrive_expect_tx(qfull, ((w.n[0] > 0) + (w.n[1] > 0)) * qbytes);
+        for (int t = 0; t < NT; ++t)
+          if (w.n[t] > 0)
             for (int c = 0; c < D / 64; ++c)
-              tma_3d(dst + c * S::half_bytes, kv ? &tv : &tk, c * 64, w.h, w.key0 + j * kTile,
-                     &full[s]);
+              tma_3d(sq + t * S::tile_bytes + c * S::half_bytes, &tq, c * 64, w.h * a.grp,
+                     w.first[t], qfull);
+      }
+      // paged: lane i brings the i-th page (or its 128 places) of a key tile;
+      // its number is asked for one tile ahead
+      const int page = 1 << a.shift, box = min(page, kTile), boxes = kTile / box;
+      auto number_of = [&](int j) -> int {
+        const long long at = (long long)w.key0 + (long long)j * kTile + lane * box;
+        if (lane >= boxes || at >= a.prefix_len || (at >> a.shift) >= a.n_prefix_pages) return -1;
+        const int x = __ldg(a.pages + (at >> a.shift));
+        return x >= a.n_pages ? -1 : x;
+      };
+      int number = PAGED ? number_of(0) : 0;
+      bool ok = true;
+      int it = 0, slot = 0;
+      uint32_t phase = 1;  // the first round finds every slot empty
+      for (int j = 0; j < n_max && ok; ++j) {
+        int x = 0, off = 0;
+        if constexpr (PAGED) {
+          // a page that is not there: past the pool, which reads as zeros, and
+          // left out of the softmax
+          const unsigned there = __ballot_sync(~0u, number >= 0);
+          if (lane == 0) {
+            uint32_t m = 0;
+            for (int i = 0; i < boxes; ++i)
+              if ((there >> i) & 1) m |= ((1u << (box / 16)) - 1) << (i * (box / 16));
+            seen_mask[j & 7] = m;
+          }
+          x = number < 0 ? a.n_pages : number;
+          off = (w.key0 + j * kTile + lane * box) & (page - 1);
+          number = number_of(j + 1);
+        }
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && mbar_wait(&empty[slot], phase, err);
+          if (!ok) break;
+          uint8_t* dst = skv + (size_t)slot * S::tile_bytes;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::tile_bytes);
+          __syncwarp();
+          if constexpr (PAGED) {
+            if (lane < boxes)
+              for (int c = 0; c < D / 64; ++c)
+                tma_4d(dst + c * S::half_bytes + lane * box * 128, &tk, c * 64, off,
+                       w.h + kv * a.Hkv, x, &full[slot]);
+          } else if (lane < D / 64) {
+            tma_3d(dst + lane * S::half_bytes, kv ? &tv : &tk, lane * 64, w.h,
+                   w.key0 + j * kTile, &full[slot]);
+          }
+          ++it;
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
       }
-      counts[0] = it;
+      if (lane == 0) counts[0] = it;
     }
     if (warp == 0 && w.fix >= 0) {
       // what lies past the keys in the last tile may be anything, and 0 * NaN
@@ -442,9 +466,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // They take turns, O += P V and the next S = Q K^T of one tile together:
     // left alone the tiles fall into step, and then both softmaxes compete for
     // the exponentials while the tensor cores wait.
-    if ((warp == 1 || warp == 2) && n_max > 0) {
+    if (warp >= 1 && warp <= NT && n_max > 0) {
       const int t = warp - 1, mine = w.n[t];
-      const uint32_t ts = tmem + t * kTile, to = tmem + 256 + t * kTile;
+      const uint32_t ts = tmem + t * kTile, to = tmem + (NT + t) * kTile;
       const uint64_t dq = kdesc(smem_u32(sq + t * S::tile_bytes)), dk = kdesc(smem_u32(skv));
       const uint64_t dv = vdesc(smem_u32(skv), S::half_bytes);
       int slot = 0, seen = 0;
@@ -489,7 +513,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int half = 0; half < 2; ++half) {
           if (j < mine) ok = ok && mbar_wait(&pfull[2 * t + half], (uint32_t)j & 1u, err);
           // (a warp without work waits too: it must not run two turns ahead)
-          if (!half && (t || j)) ok = ok && mbar_wait(&turn[t], (uint32_t)(j + t + 1) & 1u, err);
+          if (NT == 2 && !half && (t || j))
+            ok = ok && mbar_wait(&turn[t], (uint32_t)(j + t + 1) & 1u, err);
           if (j >= mine) break;
           fence_after();
           if (ok && elect_one()) {
@@ -519,7 +544,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           next_slot();
         }
-        if (lane == 0) mbar_arrive(&turn[1 - t]);
+        if (NT == 2 && lane == 0) mbar_arrive(&turn[1 - t]);
       }
       if (!ok && elect_one()) {  // this thread's MMAs finish before the memory goes away
         mma_commit(&drain[t]);
@@ -533,7 +558,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // --------------------------------------------------------- softmax --
     const int t = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t base = tmem + ((uint32_t)(q * 32) << 16);
-    const uint32_t ts = base + t * kTile, to = base + 256 + t * kTile;
+    const uint32_t ts = base + t * kTile, to = base + (NT + t) * kTile;
     const int tok = row / a.grp, head = w.h * a.grp + row % a.grp, tiles = w.n[t];
     const bool mine = tok < w.count[t] && row < a.grp * a.tpt;
     // keys this row attends to, counted from key0
@@ -670,7 +695,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // copies asked for but never seen (only after a failed wait): let them land
     for (long long k = 0; k < kSpinLimit && !mbar_try_wait(qfull, 0); ++k) {
     }
-    for (int i = min(counts[1], counts[2]); i < counts[0]; ++i)
+    for (int i = NT == 2 ? min(counts[1], counts[2]) : counts[1]; i < counts[0]; ++i)
       for (long long k = 0; k < kSpinLimit && !mbar_try_wait(&full[i % NS], (uint32_t)(i / NS) & 1u);
            ++k) {
       }
@@ -678,7 +703,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   if (warp == 1) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(S::columns)
                  : "memory");
   }
 }
@@ -724,6 +750,7 @@ template <int D, int F16>
 __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs a) {
   constexpr int ROWB = D * 2, KS = D / 16, NTO = D / 8, CH = D / 8;
   extern __shared__ __align__(128) uint8_t own_raw[];
+  pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   int x = blockIdx.x;
@@ -741,6 +768,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   const size_t id0 = (size_t)split * rows + (size_t)b * a.Hq + g * a.grp + mt * 16;
   if (t0 >= t1) {
     if (tid < heads) a.part_ml[id0 + tid] = make_float2(-INFINITY, 0.0f);
+    if (blockIdx.x == 0) pdl_wait();
     return;
   }
   uint8_t* ring = own_raw + (size_t)warp * kOwnStages * 2 * kOwnTile * ROWB;
@@ -916,10 +944,14 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
     }
     if (lane == 0) a.part_ml[id0 + r] = make_float2(mm, ll);
   }
+  // The launch before this one is the prefix, beside which this one ran.  One
+  // CTA waits for its end, so that the end of this launch is that of both.
+  if (blockIdx.x == 0) pdl_wait();
 }
 
 // ------------------------------------------------------------------ join ---
-// One warp per (row, query head): the parts' (max, sum, unnormalised o).
+// One CTA per (row, query head): the parts' (max, sum, unnormalised o).  Its
+// D / 4 lanes a part, the parts side by side, then one sum over those.
 struct JoinArgs {
   const float* part_o;
   const float2* part_ml;
@@ -930,38 +962,81 @@ struct JoinArgs {
   int n_rows, Hq, parts;
 };
 
+constexpr int kJoinThreads = 128;
+constexpr int kMaxParts = 256;
+
 template <int D, int F16>
-__global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs a) {
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const long long rows = (long long)a.n_rows * a.Hq;
-  if (id >= rows) return;
-  const int b = (int)(id / a.Hq), h = (int)(id % a.Hq);
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const JoinArgs a) {
+  constexpr int W = D / 4, SIDE = kJoinThreads / W;  // lanes per part, parts side by side
+  __shared__ float f[kMaxParts];
+  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ float4 acc[SIDE][W];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
+  const size_t id = blockIdx.x, rows = (size_t)a.n_rows * a.Hq;
+  pdl_wait();
   if (a.lens[b] < 0) return;  // padding
   float m = -INFINITY;
-  for (int p = lane; p < a.parts; p += 32) m = fmaxf(m, a.part_ml[p * rows + id].x);
+  float2 ml[kMaxParts / kJoinThreads];
+#pragma unroll
+  for (int i = 0; i < kMaxParts / kJoinThreads; ++i) {
+    const int p = tid + i * kJoinThreads;
+    ml[i] = p < a.parts ? __ldcg(a.part_ml + p * rows + id) : make_float2(-INFINITY, 0.0f);
+    m = fmaxf(m, ml[i].x);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  float l = 0.0f, y[V];
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < V; ++i) y[i] = 0.0f;
-  for (int p = 0; p < a.parts; ++p) {
-    const float2 ml = a.part_ml[p * rows + id];
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // no key: its o was not written
-    const float f = ex2(ml.x - m);
-    l += ml.y * f;
-    const float* src = a.part_o + (p * rows + id) * D + lane * V;
+  for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, red[0][k]);
+  float l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] += src[i] * f;
+  for (int i = 0; i < kMaxParts / kJoinThreads; ++i) {
+    const int p = tid + i * kJoinThreads;
+    if (p < a.parts) {
+      // a part without a key has no o
+      const float x = ml[i].x == -INFINITY && ml[i].y == 0.0f ? 0.0f : ex2(ml[i].x - m);
+      f[p] = x;
+      if (x != 0.0f) l += ml[i].y * x;
+    }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* dst = a.out + (int64_t)b * a.o_row + (int64_t)h * a.o_head + lane * V;
 #pragma unroll
-  for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) =
-        l == 0.0f ? 0u : pack2<F16>(y[i] * inv, y[i + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[id] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) l += red[1][k];
+  const int side = tid / W, d = (tid % W) * 4;
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int p = side; p < a.parts; p += SIDE) {
+    const float x = f[p];
+    if (x == 0.0f) continue;
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (p * rows + id) * D + d));
+    y.x += v.x * x;
+    y.y += v.y * x;
+    y.z += v.z * x;
+    y.w += v.w * x;
+  }
+  acc[side][tid % W] = y;
+  __syncthreads();
+  if (tid < W) {
+#pragma unroll
+    for (int k = 1; k < SIDE; ++k) {
+      const float4 v = acc[k][tid];
+      y.x += v.x;
+      y.y += v.y;
+      y.z += v.z;
+      y.w += v.w;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint2 o = make_uint2(0u, 0u);
+    if (l != 0.0f) o = make_uint2(pack2<F16>(y.x * inv, y.y * inv), pack2<F16>(y.z * inv, y.w * inv));
+    *reinterpret_cast<uint2*>(a.out + (int64_t)b * a.o_row + (int64_t)h * a.o_head + d) = o;
+    if (tid == 0 && a.lse) a.lse[id] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
 }
 
 // ------------------------------------------------------------------ host ---
@@ -1008,49 +1083,61 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
   if (e != cudaSuccess) return e;
   if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  // all of the SM's memory as shared memory, or two kernels' CTAs could not
+  // stand side by side on it
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
   return e;
 }
 
-template <int D, int F16, bool PAGED>
+template <int D, int F16, bool PAGED, int NT>
 cudaError_t launch_tc_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const AttnTcArgs& a, unsigned grid, cudaStream_t st) {
+  using S = TcShape<D, NT>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(attn_tc_kernel<D, F16, PAGED>, TcShape<D>::smem, done);
+  const cudaError_t e = allow_smem(attn_tc_kernel<D, F16, PAGED, NT>, S::smem, done);
   if (e != cudaSuccess) return e;
-  attn_tc_kernel<D, F16, PAGED><<<grid, kTcThreads, TcShape<D>::smem, st>>>(tq, tk, tv, a);
+  attn_tc_kernel<D, F16, PAGED, NT><<<grid, S::threads, S::smem, st>>>(tq, tk, tv, a);
   return cudaGetLastError();
+}
+
+template <bool PAGED, int NT>
+cudaError_t launch_tc_n(int D, int f16, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, const AttnTcArgs& a, unsigned grid, cudaStream_t st) {
+  if (D == 128)
+    return f16 ? launch_tc_t<128, 1, PAGED, NT>(tq, tk, tv, a, grid, st)
+               : launch_tc_t<128, 0, PAGED, NT>(tq, tk, tv, a, grid, st);
+  return f16 ? launch_tc_t<64, 1, PAGED, NT>(tq, tk, tv, a, grid, st)
+             : launch_tc_t<64, 0, PAGED, NT>(tq, tk, tv, a, grid, st);
 }
 
 template <bool PAGED>
-cudaError_t launch_tc(int D, int f16, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_tc(int nt, int D, int f16, const CUtensorMap& tq, const CUtensorMap& tk,
                       const CUtensorMap& tv, const AttnTcArgs& a, unsigned grid, cudaStream_t st) {
-  if (D == 128)
-    return f16 ? launch_tc_t<128, 1, PAGED>(tq, tk, tv, a, grid, st)
-               : launch_tc_t<128, 0, PAGED>(tq, tk, tv, a, grid, st);
-  return f16 ? launch_tc_t<64, 1, PAGED>(tq, tk, tv, a, grid, st)
-             : launch_tc_t<64, 0, PAGED>(tq, tk, tv, a, grid, st);
+  return nt == 2 ? launch_tc_n<PAGED, 2>(D, f16, tq, tk, tv, a, grid, st)
+                 : launch_tc_n<PAGED, 1>(D, f16, tq, tk, tv, a, grid, st);
 }
 
 template <int D, int F16>
-cudaError_t launch_own_t(const OwnArgs& a, const JoinArgs& j, cudaStream_t st) {
+cudaError_t launch_own_t(const OwnArgs& a, const JoinArgs& j, bool after_prefix, cudaStream_t st) {
   if (a.splits > 0) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(attn_own_kernel<D, F16>, own_smem<D>(), done);
-    if (e != cudaSuccess) return e;
+    cudaError_t e = allow_smem(attn_own_kernel<D, F16>, own_smem<D>(), done);
     const unsigned grid = (unsigned)((long long)a.n_rows * a.Hkv * a.mtiles * a.splits);
-    attn_own_kernel<D, F16><<<grid, kOwnWarps * 32, own_smem<D>(), st>>>(a);
-    const cudaError_t e2 = cudaGetLastError();
-    if (e2 != cudaSuccess) return e2;
+    if (e == cudaSuccess)
+      e = launch_ex(attn_own_kernel<D, F16>, dim3(grid), dim3(kOwnWarps * 32), own_smem<D>(), st,
+                    after_prefix, a);
+    if (e != cudaSuccess) return e;
   }
-  attn_join_kernel<D, F16>
-      <<<(unsigned)(((long long)j.n_rows * j.Hq + 3) / 4), 128, 0, st>>>(j);
-  return cudaGetLastError();
+  return launch_ex(attn_join_kernel<D, F16>, dim3((unsigned)(j.n_rows * j.Hq)), dim3(kJoinThreads),
+                   0, st, after_prefix || a.splits > 0, j);
 }
 
 // How m3_attn_prefix splits its work; the workspace follows from it.
 struct PrefixPlan {
-  int grp = 0, tpt = 0, units = 0;       // rows per tile, pairs of row tiles
+  int grp = 0, tpt = 0, nt = 0, units = 0;  // rows per row tile, row tiles of a CTA, such groups
   int pre_splits = 0, pre_tiles = 0;     // splits of the prefix, key tiles of each
   int mtiles = 0, own_splits = 0;
   int64_t rows = 0, bytes = 0;
@@ -1067,13 +1154,15 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
   const int nsm = sm_count();
   p->grp = Hq / Hkv;
   p->tpt = kTile / p->grp;
-  p->units = (n_rows + 2 * p->tpt - 1) / (2 * p->tpt);
+  p->nt = n_rows > p->tpt ? 2 : 1;
+  p->units = (n_rows + p->nt * p->tpt - 1) / (p->nt * p->tpt);
   p->rows = (int64_t)n_rows * Hq;
   const long long key_tiles = (prefix + kTile - 1) / kTile;
   if (key_tiles > 0) {
     // one round of CTAs over the SMs (a CTA fills one), whole key tiles
     long long s = nsm / ((long long)p->units * Hkv);
     s = s < 1 ? 1 : s > key_tiles ? key_tiles : s;
+    s = s > kMaxParts - 64 ? kMaxParts - 64 : s;
     p->pre_tiles = (int)((key_tiles + s - 1) / s);
     p->pre_splits = (int)((key_tiles + p->pre_tiles - 1) / p->pre_tiles);
   }
@@ -1088,7 +1177,7 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
   const int64_t parts = p->pre_splits + p->own_splits;
   p->bytes = ((parts * p->rows * 8 + 15) & ~(int64_t)15) + parts * p->rows * D * 4;
   if (p->bytes == 0) p->bytes = 16;
-  return (long long)p->units * Hkv * p->pre_splits <= INT_MAX &&
+  return p->rows <= INT_MAX && (long long)p->units * Hkv * p->pre_splits <= INT_MAX &&
          (long long)n_rows * Hkv * p->mtiles * p->own_splits <= INT_MAX;
 }
 
@@ -1156,10 +1245,12 @@ extern "C" int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, in
                            n_k ? v_token : q_token, n_k ? v_head : q_head, 1, kTile);
   if (!ok) return set_error(M3_EINVAL, "no tensor map for these strides");
   // every sequence's last unit may be short: at most one more unit each
-  const long long span = 2 * a.tpt;
-  const long long units = n_q / span + (n_seq < n_q ? n_seq : n_q);
+  auto most = [&](int nt) { return n_q / (nt * a.tpt) + (n_seq < n_q ? n_seq : n_q); };
+  // one row tile per CTA where pairs would leave half of the SMs without work
+  const int nt = (long long)most(2) * Hkv * 2 <= sm_count() ? 1 : 2;
+  const long long units = most(nt);
   if (units * Hkv > INT_MAX) return set_error(M3_EINVAL, "too many tokens");
-  OPS_CK(launch_tc<false>(D, f16, tq, tk, tv, a, (unsigned)(units * Hkv),
+  OPS_CK(launch_tc<false>(nt, D, f16, tq, tk, tv, a, (unsigned)(units * Hkv),
                           static_cast<cudaStream_t>(cuda_stream)));
   return M3_OK;
 }
@@ -1236,7 +1327,7 @@ extern "C" int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, con
     if (!make_rows_map(&tq, f16, q, n_rows, Hq, D, q_row, q_head, a.grp, a.tpt) ||
         !make_map(&tk, f16, 4, pool, dims, strides, box))
       return set_error(M3_EINVAL, "no tensor map for these strides");
-    OPS_CK(launch_tc<true>(D, f16, tq, tk, tk, a, (unsigned)(p.units * Hkv * pre), st));
+    OPS_CK(launch_tc<true>(p.nt, D, f16, tq, tk, tk, a, (unsigned)(p.units * Hkv * pre), st));
   }
   OwnArgs o{};
   o.q = static_cast<const uint16_t*>(q);
@@ -1260,9 +1351,9 @@ extern "C" int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, con
   o.part_ml = ml + (int64_t)pre * p.rows;
   JoinArgs j{po, ml, lens, static_cast<uint16_t*>(out), o_row, o_head, lse, n_rows, Hq, (int)parts};
   if (D == 128)
-    OPS_CK(f16 ? (launch_own_t<128, 1>(o, j, st)) : (launch_own_t<128, 0>(o, j, st)));
+    OPS_CK(f16 ? (launch_own_t<128, 1>(o, j, pre > 0, st)) : (launch_own_t<128, 0>(o, j, pre > 0, st)));
   else
-    OPS_CK(f16 ? (launch_own_t<64, 1>(o, j, st)) : (launch_own_t<64, 0>(o, j, st)));
+    OPS_CK(f16 ? (launch_own_t<64, 1>(o, j, pre > 0, st)) : (launch_own_t<64, 0>(o, j, pre > 0, st)));
   return M3_OK;
 }
 

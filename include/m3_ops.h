@@ -126,10 +126,10 @@ M3_API int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, const v
  *   x -= frequency * c + (c > 0 ? presence : 0)
  *   x += the row's biases of token i, added in their order
  *   x = -inf where the grammar does not allow token i
- *  history [n_rows][ld_history] int32, n_history (up to 524287) per row, of
+ *  history [n_rows][ld_history] int32, n_history (up to 2^24) per row, of
  *    which the first hist_len[r] count (nullable: all); numbers outside the vocabulary do not.
  *  repetition (> 0), frequency, presence: fp32 [n_rows], nullable (1, 0, 0).
- *  bias_ids int32, bias fp32: [n_rows][n_bias], up to 4095; ids outside the
+ *  bias_ids int32, bias fp32: [n_rows][n_bias], up to 4096; ids outside the
  *    vocabulary are skipped.
  *  mask uint32 [n_masks][ceil(vocab / 32)]: bit i % 32 of word i / 32 set:
  *    allowed.  mask_row [n_rows]: the mask of each row, outside 0..n_masks - 1:

@@ -59,7 +59,7 @@ def check_map(ops, fresh, cached, free, table, page, n_pages, start=0, pad=0, fr
 
 @pytest.mark.parametrize("n,most_fresh,most_cached,page", [
     (1, 1, 0, 16), (1, 0, 0, 16), (3, 40, 100, 16), (16, 1, 9000, 256), (33, 300, 70, 32), (257, 90, 600, 64),
-    (1000, 5, 0, 1024), (8192, 3, 50, 128)])
+    (1000, 5, 0, 1024), (5119, 2, 3, 16), (6143, 2, 3, 16), (8192, 3, 50, 128)])
 @pytest.mark.parametrize("pad", [0, 5])
 def test_map(ops, n, most_fresh, most_cached, page, pad):
     rnd = random.Random(n * 7 + page)
@@ -395,7 +395,8 @@ def rule_inputs(r, n, nh, nb, nm, seed):
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("r,n,nh,nb,nm", [(1, 1, 1, 1, 1), (2, 16385, 1500, 16, 1), (3, 31, 9, 40, 2), (5, 1000, 0, 7, 0),
-                                          (4, 4097, 70, 0, 3), (700, 8191, 33, 5, 4), (2, 50001, 4096, 300, 2)])
+                                          (4, 4097, 70, 0, 3), (700, 8191, 33, 5, 4), (300, 20000, 50, 0, 0),
+                                          (300, 20000, 0, 9, 0), (300, 20001, 0, 0, 2), (2, 50001, 4096, 300, 2)])
 def test_rules(ops, r, n, nh, nb, nm, dtype):
     x = (4 * torch.randn(r, n, generator=gen(n), device="cuda")).to(dtype)
     history, hist_len, rep, freq, pres, ids, bias, mask, row = rule_inputs(r, n, nh, nb, nm, n + r)

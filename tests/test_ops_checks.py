@@ -107,7 +107,7 @@ RULES = dict(dtype=0, n=2, vocab=100, x=P, ldx=100, out=P, ldo=100, hist=P, nh=5
              pres=None, ids=P, bias=P, nb=3, mask=P, nm=2, mr=None, stream=None)
 
 
-@pytest.mark.parametrize("bad", [dict(dtype=3), dict(n=-1), dict(vocab=0), dict(x=None), dict(out=None), dict(nb=4096), dict(nh=1 << 19, ldh=1 << 19),
+@pytest.mark.parametrize("bad", [dict(dtype=3), dict(n=-1), dict(vocab=0), dict(x=None), dict(out=None), dict(nb=4097), dict(nh=(1 << 24) + 1, ldh=1 << 25),
                                  dict(nb=-1), dict(ids=None), dict(bias=None), dict(hist=None), dict(nh=-1), dict(ldx=99),
                                  dict(ldo=99), dict(ldh=4), dict(nm=0), dict(nm=3), dict(out=P + 400), dict(x=P + 2),
                                  dict(out=P, ldo=104)])
