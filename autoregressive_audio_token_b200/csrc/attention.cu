@@ -90,6 +90,20 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int D, int kv_f16, int T, cud
   return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_packed_qkv(const PackedQkvArgs& a, int D, int kv_f16, cudaStream_t st) {
+  const unsigned grid = (unsigned)(((long long)a.T * (a.Hq + 2 * a.Hkv) + 7) / 8);
+  if (D == 128) {
+    if (kv_f16) packed_qkv_kernel<128, 1><<<grid, 256, 0, st>>>(a);
+    else packed_qkv_kernel<128, 0><<<grid, 256, 0, st>>>(a);
+  } else if (D == 64) {
+    if (kv_f16) packed_qkv_kernel<64, 1><<<grid, 256, 0, st>>>(a);
+    else packed_qkv_kernel<64, 0><<<grid, 256, 0, st>>>(a);
+  } else {
+    return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
 cudaError_t launch_attn(const AttnArgs& a, int D, int kv_f16, int splits, int rows,
                         cudaStream_t st, bool pdl) {
   if (D == 128) return kv_f16 ? launch_attn_t<128, 1>(a, splits, rows, st, pdl)

@@ -316,4 +316,71 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AttnArgs a, int T)
   }
 }
 
+// The same for packed prompts of several cache rows, whose attention reads q, k
+// and v from the projection's output itself: one warp per (token, head slot).
+// q and k are normalised, rotated and rounded in place; k and v also go to the
+// token's row and position of the cache.
+struct PackedQkvArgs {
+  __nv_bfloat16* qkv;  // [T][ldqkv]: q | k | v
+  int ldqkv;
+  const __nv_bfloat16* q_norm;
+  const __nv_bfloat16* k_norm;
+  float eps;
+  const float2* rope;               // [T][D / 2]
+  const unsigned long long* pages;  // [cache rows][n_layers][max_pages]
+  int layer, n_layers, max_pages, page_size;
+  int Hq, Hkv, T;
+  const int32_t* seqs;       // [T] which prompt
+  const int32_t* positions;  // [T]
+  const int32_t* rows;       // [prompts] its cache row
+};
+
+template <int D, int KVF16>
+__global__ void __launch_bounds__(256) packed_qkv_kernel(const PackedQkvArgs a) {
+  constexpr int VPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int slots = a.Hq + 2 * a.Hkv;
+  if (item >= (long long)a.T * slots) return;
+  const int t = (int)(item / slots), s = (int)(item % slots);
+  __nv_bfloat16* src = a.qkv + (size_t)t * a.ldqkv + (size_t)s * D;
+  float v[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] = __bfloat162float(src[lane + 32 * i]);
+  if (s < a.Hq + a.Hkv) {
+    const __nv_bfloat16* gain = s < a.Hq ? a.q_norm : a.k_norm;
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      v[i] = round_bf16(__bfloat162float(gain[lane + 32 * i]) * round_bf16(v[i] * inv));
+#pragma unroll
+    for (int i = 0; i < VPL / 2; ++i) {
+      const float2 cs = a.rope[(size_t)t * (D / 2) + lane + 32 * i];
+      const float x0 = v[i], x1 = v[i + VPL / 2];
+      v[i] = __fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y));
+      v[i + VPL / 2] = __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y));
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = round_bf16(v[i]);
+      src[lane + 32 * i] = __float2bfloat16_rn(v[i]);
+    }
+  }
+  if (s >= a.Hq) {  // K heads, then V heads, as in a page
+    const int pos = a.positions[t], row = a.rows[a.seqs[t]];
+    const unsigned long long* pt =
+        a.pages + ((size_t)row * a.n_layers + a.layer) * a.max_pages;
+    uint16_t* base = reinterpret_cast<uint16_t*>(pt[pos / a.page_size]);
+    const int off = pos % a.page_size;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      base[kv_elem_offset(s - a.Hq, a.page_size, off, D, lane + 32 * i)] = f32_to_kv<KVF16>(v[i]);
+  }
+}
+
 }  // namespace m3

@@ -70,6 +70,10 @@ cudaError_t launch_attn(const AttnArgs& a, int D, int kv_f16, int splits, int ro
 // a.fixed_pos .. + T - 1 (attn_prefill.cuh): their K/V appended to the row's
 // cache, then the tiled attention.
 cudaError_t launch_attn_prefill(const AttnArgs& a, int D, int kv_f16, int T, cudaStream_t st);
+// The q, k and v of packed prompts made ready in place, k and v appended to
+// their rows' caches (attn_prefill.cuh); their attention is attn_prompt's.
+struct PackedQkvArgs;
+cudaError_t launch_packed_qkv(const PackedQkvArgs& a, int D, int kv_f16, cudaStream_t st);
 
 // The prefill's tensor-core GEMM (gemm_tc.cu, tcgen05 with tensor-memory
 // accumulators): Y[t][o] = sum_k W[o][k] X[t][k] for T tokens, W in the tiled

@@ -14,7 +14,10 @@
 #include <vector>
 
 #include "m3.h"
+#include "m3_ops.h"
+#include "attn_prefill.cuh"
 #include "launch.cuh"
+#include "ops.cuh"
 #include "misc.cuh"
 #include "gemv_tile.cuh"
 #include "dit_gemm.cuh"
@@ -180,6 +183,11 @@ struct m3_ctx {
   int pf_chunk = 0;
   bf16 *pf_x = nullptr, *pf_n = nullptr, *pf_qkv = nullptr, *pf_o = nullptr, *pf_act = nullptr;
   float2* pf_rope = nullptr;       // [pf_chunk][head_dim / 2]
+  // packed prompts (m3_prefill_rows): per token its prompt, position and slot,
+  // per prompt its length, cache row and first token
+  int32_t *pr_seqs = nullptr, *pr_pos = nullptr, *pr_ints = nullptr;
+  int64_t* pr_slots = nullptr;
+  int pr_cap = 0;                  // prompts pr_ints holds
   // the prefill GEMM's operands: a row-major copy of each bf16 layer's
   // projections (qkv | o | gate/up interleaved | down), made at the first
   // GEMM prefill from the tiled weights; stale once the layer is reloaded
@@ -1306,7 +1314,14 @@ static int ensure_prefill_copies(m3_ctx* c) {
   return M3_OK;
 }
 
-static int record_prefill_layer(m3_ctx* c, const DLayer& L, int T, int p0, int layer) {
+// The packed prompts of one m3_prefill_rows pass.
+struct PackedPrompts {
+  int n;
+  const int32_t *cu, *rows;  // [n + 1] first tokens, [n] cache rows
+};
+
+static int record_prefill_layer(m3_ctx* c, const DLayer& L, int T, int p0, int layer,
+                                const PackedPrompts* packed = nullptr) {
   const m3_config& g = c->cfg;
   const int H = g.hidden, d = g.head_dim, ldqkv = (g.n_q_heads + 2 * g.n_kv_heads) * d;
   const int hq = g.n_q_heads * d;
@@ -1371,7 +1386,32 @@ static int record_prefill_layer(m3_ctx* c, const DLayer& L, int T, int p0, int l
   at.pos_stride = 1;
   at.err = c->err;
   const int grp = g.n_q_heads / g.n_kv_heads;
-  if ((d == 64 || d == 128) && 16 % grp == 0 && c->bucket % 32 == 0) {
+  if (packed) {
+    PackedQkvArgs pa{};
+    pa.qkv = c->pf_qkv;
+    pa.ldqkv = ldqkv;
+    pa.q_norm = L.q_norm;
+    pa.k_norm = L.k_norm;
+    pa.eps = g.rms_eps;
+    pa.rope = c->pf_rope;
+    pa.pages = c->d_pages;
+    pa.layer = layer;
+    pa.n_layers = g.n_layers;
+    pa.max_pages = c->max_pages;
+    pa.page_size = c->bucket;
+    pa.Hq = g.n_q_heads;
+    pa.Hkv = g.n_kv_heads;
+    pa.T = T;
+    pa.seqs = c->pr_seqs;
+    pa.positions = c->pr_pos;
+    pa.rows = packed->rows;
+    CK(launch_packed_qkv(pa, d, c->kv_f16, c->st));
+    // bf16 whatever the cache holds: f16 keeps every bf16 value it can represent
+    const bf16 *k = c->pf_qkv + hq, *v = k + (size_t)g.n_kv_heads * d;
+    CKR(attn_prompt(M3_KV_BF16, packed->n, T, T, g.n_q_heads, g.n_kv_heads, d, c->pf_qkv, ldqkv, d,
+                    k, ldqkv, d, v, ldqkv, d, packed->cu, nullptr, 1.0f / sqrtf((float)d), c->pf_o,
+                    hq, d, nullptr, c->err, c->st));
+  } else if ((d == 64 || d == 128) && 16 % grp == 0 && c->bucket % 32 == 0) {
     // the chunk's K/V appended, then the tiled causal attention in which the
     // chunk's tokens share every K/V tile
     CK(launch_attn_prefill(at, d, c->kv_f16, T, c->st));
@@ -1409,6 +1449,20 @@ static bool prefill_tc_ok(const m3_ctx* c) {
   return true;
 }
 
+// The activation buffers of a GEMM prefill pass, of pf_chunk tokens.
+static int ensure_prefill_buffers(m3_ctx* c) {
+  const m3_config& g = c->cfg;
+  const int P = c->pf_chunk, H = g.hidden, d = g.head_dim;
+  const int ldqkv = (g.n_q_heads + 2 * g.n_kv_heads) * d;
+  if (!c->pf_x) CKR(dalloc(c, &c->pf_x, sizeof(bf16) * P * H));
+  if (!c->pf_n) CKR(dalloc(c, &c->pf_n, sizeof(bf16) * P * H));
+  if (!c->pf_qkv) CKR(dalloc(c, &c->pf_qkv, sizeof(bf16) * P * ldqkv));
+  if (!c->pf_o) CKR(dalloc(c, &c->pf_o, sizeof(bf16) * P * g.n_q_heads * d));
+  if (!c->pf_act) CKR(dalloc(c, &c->pf_act, sizeof(bf16) * P * g.ffn));
+  if (!c->pf_rope) CKR(dalloc(c, &c->pf_rope, sizeof(float2) * P * (d / 2)));
+  return M3_OK;
+}
+
 extern "C" int m3_prefill(m3_ctx* c, int row, int start, int n_tokens, const void* x,
                           void* h_last) {
   if (!c || !x) return fail(M3_EINVAL, "null argument");
@@ -1441,15 +1495,8 @@ extern "C" int m3_prefill(m3_ctx* c, int row, int start, int n_tokens, const voi
   CK(cudaStreamSynchronize(c->st));  // the host staging of the page table
   const bf16* xs = static_cast<const bf16*>(x);
   if (tc) {
-    const int H = g.hidden, d = g.head_dim, ldqkv = (g.n_q_heads + 2 * g.n_kv_heads) * d;
-    if (!c->pf_x) {
-      CKR(dalloc(c, &c->pf_x, sizeof(bf16) * P * H));
-      CKR(dalloc(c, &c->pf_n, sizeof(bf16) * P * H));
-      CKR(dalloc(c, &c->pf_qkv, sizeof(bf16) * P * ldqkv));
-      CKR(dalloc(c, &c->pf_o, sizeof(bf16) * P * g.n_q_heads * d));
-      CKR(dalloc(c, &c->pf_act, sizeof(bf16) * P * g.ffn));
-      CKR(dalloc(c, &c->pf_rope, sizeof(float2) * P * (d / 2)));
-    }
+    const int H = g.hidden, d = g.head_dim;
+    CKR(ensure_prefill_buffers(c));
     if (c->wdtype == M3_W_BF16 && prefill_gemm_shapes_ok(g)) CKR(ensure_prefill_copies(c));
     for (int c0 = 0; c0 < n_tokens; c0 += P) {
       const int T = n_tokens - c0 < P ? n_tokens - c0 : P;
@@ -1500,6 +1547,92 @@ extern "C" int m3_prefill(m3_ctx* c, int row, int start, int n_tokens, const voi
     }
   }
   return leave(c);
+}
+
+// Whether packed passes take this context's prompts: the GEMM prefill over the
+// row-major bf16 weights, and m3_attn_prompt's shapes and alignment.
+static bool packed_ok(const m3_ctx* c) {
+  const m3_config& g = c->cfg;
+  return c->wdtype == M3_W_BF16 && prefill_tc_ok(c) && prefill_gemm_shapes_ok(g) &&
+         (g.head_dim == 64 || g.head_dim == 128) && g.n_q_heads % g.n_kv_heads == 0 &&
+         g.n_q_heads / g.n_kv_heads <= 64;
+}
+
+extern "C" int m3_prefill_rows(m3_ctx* c, int n_rows, const int32_t* rows,
+                               const int32_t* n_tokens, const void* x, void* h_last) {
+  if (!c || !rows || !n_tokens || !x) return fail(M3_EINVAL, "null argument");
+  const m3_config& g = c->cfg;
+  if (!c->d_pages) return fail(M3_ESTATE, "m3_kv_alloc first");
+  for (int l = 0; l < g.n_layers; ++l)
+    if (!c->loaded[l]) return fail(M3_ESTATE, "layer " + std::to_string(l) + " not loaded");
+  if (h_last && !c->final_norm) return fail(M3_ESTATE, "final norm not loaded");
+  if (n_rows < 1 || n_rows > c->kv_rows) return fail(M3_EINVAL, "n_rows out of 1..cache rows");
+  std::vector<char> seen(c->kv_rows, 0);
+  int longest = 0;
+  for (int i = 0; i < n_rows; ++i) {
+    if (rows[i] < 0 || rows[i] >= c->kv_rows || seen[rows[i]]) return fail(M3_EINVAL, "rows");
+    seen[rows[i]] = 1;
+    if (n_tokens[i] < 1) return fail(M3_EINVAL, "n_tokens");
+    if (n_tokens[i] > c->kv_max_pos) return fail(M3_ECAPACITY, "n_tokens outside the KV capacity");
+    longest = n_tokens[i] > longest ? n_tokens[i] : longest;
+  }
+  const int H = g.hidden, d = g.head_dim;
+  const bf16* xs = static_cast<const bf16*>(x);
+  bf16* hs = static_cast<bf16*>(h_last);
+  const bool packs = packed_ok(c);
+  if (packs) {
+    if (c->pf_chunk == 0) c->pf_chunk = 2048;
+    CKR(enter(c));
+    CKR(ensure_pages(c, longest));
+    CKR(ensure_prefill_buffers(c));
+    CKR(ensure_prefill_copies(c));
+    const int P = c->pf_chunk;
+    if (!c->pr_seqs) CKR(dalloc(c, &c->pr_seqs, sizeof(int32_t) * P));
+    if (!c->pr_pos) CKR(dalloc(c, &c->pr_pos, sizeof(int32_t) * P));
+    if (!c->pr_slots) CKR(dalloc(c, &c->pr_slots, sizeof(int64_t) * P));
+    if (c->pr_cap < n_rows) {  // lengths, rows, first tokens (n + 1), sums, one word
+      CKR(dalloc(c, &c->pr_ints, sizeof(int32_t) * (4 * (size_t)c->kv_rows + 2)));
+      c->pr_cap = c->kv_rows;
+    }
+    CK(cudaMemcpyAsync(c->pr_ints, n_tokens, sizeof(int32_t) * n_rows, cudaMemcpyHostToDevice, c->st));
+    CK(cudaMemcpyAsync(c->pr_ints + c->pr_cap, rows, sizeof(int32_t) * n_rows, cudaMemcpyHostToDevice,
+                       c->st));
+    CK(cudaStreamSynchronize(c->st));  // the caller's arrays
+  }
+  for (int i = 0; i < n_rows;) {
+    // the next prompts that fit one pass; one that does not goes by itself
+    int n = 0, T = 0;
+    while (packs && i + n < n_rows && n < 8192 && T + n_tokens[i + n] <= c->pf_chunk)
+      T += n_tokens[i + n++];
+    if (n == 0) {
+      CKR(m3_prefill(c, rows[i], 0, n_tokens[i], xs, hs ? hs + (size_t)i * H : nullptr));
+      xs += (size_t)n_tokens[i++] * H;
+      continue;
+    }
+    CKR(enter(c));
+    CK(cudaMemcpyAsync(c->pf_x, xs, sizeof(bf16) * T * H, cudaMemcpyDeviceToDevice, c->st));
+    // which prompt and position each token is
+    int32_t *lens = c->pr_ints + i, *cu = c->pr_ints + 2 * c->pr_cap, *sums = cu + c->pr_cap + 1;
+    CKR(m3_kv_map(n, lens, nullptr, nullptr, 0, nullptr, nullptr, 0, 0, 16, 0, 0, T, cu, c->pr_pos,
+                  c->pr_slots, c->pr_seqs, sums, sums + c->pr_cap, c->st));
+    rope_tokens_kernel<<<(T * (d / 2) + 255) / 256, 256, 0, c->st>>>(c->inv_freq, d / 2, c->pr_pos,
+                                                                      T, c->pf_rope);
+    CK(cudaGetLastError());
+    const PackedPrompts packed{n, cu, c->pr_ints + c->pr_cap + i};
+    for (int l = 0; l < g.n_layers; ++l) CKR(record_prefill_layer(c, c->L[l], T, 0, l, &packed));
+    int end = 0;
+    for (int k = 0; k < n; ++k) {
+      end += n_tokens[i + k];
+      if (!hs) continue;
+      rmsnorm_rows_kernel<<<1, 256, 0, c->st>>>(c->pf_x + (size_t)(end - 1) * H, c->final_norm,
+                                                g.rms_eps, H, hs + (size_t)(i + k) * H);
+      CK(cudaGetLastError());
+    }
+    CKR(leave(c));
+    xs += (size_t)T * H;
+    i += n;
+  }
+  return M3_OK;
 }
 
 // ------------------------------------------------------ generation loop ----

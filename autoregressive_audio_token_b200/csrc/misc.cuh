@@ -42,6 +42,15 @@ __global__ void rope_positions_kernel(const double* __restrict__ inv_freq, int h
   }
 }
 
+// The same for positions given one by one.
+__global__ void rope_tokens_kernel(const double* __restrict__ inv_freq, int half,
+                                   const int32_t* __restrict__ positions, int n, float2* table) {
+  for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < n * half; k += gridDim.x * blockDim.x) {
+    const double ang = (double)positions[k / half] * inv_freq[k % half];
+    table[k] = make_float2((float)cos(ang), (float)sin(ang));
+  }
+}
+
 // int8 weight-only quantisation ("MiniMax Music 3 on Metal", section
 // "Precision": one scale per row for the body and lm_head, per group of 128
 // for the depth decoder, quantised on the GPU at load):

@@ -92,6 +92,7 @@ struct AttnTcArgs {
   // both
   int Hq, Hkv, grp, tpt;  // query heads per KV head; tokens (rows) per row tile
   float c;                // scale * log2 e
+  int* err;               // where a wait that gives up says so; null: this file's word
 };
 
 __device__ __forceinline__ uint64_t kdesc(uint32_t addr) {
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(384, 1)  // 168 registers, with one row tile (
   __shared__ int have_work;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int* err = &g_ops_err;
+  int* err = a.err ? a.err : &g_ops_err;
   if (warp == 0) {
     TcWork k;
     bool some;
@@ -1200,12 +1201,11 @@ using namespace m3;
       return set_error(M3_ECUDA, std::string(#call) + ": " + cudaGetErrorString(e_)); \
   } while (0)
 
-extern "C" int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int D,
-                              const void* q, int64_t q_token, int64_t q_head, const void* k,
-                              int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
-                              int64_t v_head, const int32_t* cu_q, const int32_t* cu_k,
-                              float scale, void* out, int64_t o_token, int64_t o_head, float* lse,
-                              void* cuda_stream) {
+int m3::attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int D, const void* q,
+                    int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                    int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                    const int32_t* cu_q, const int32_t* cu_k, float scale, void* out,
+                    int64_t o_token, int64_t o_head, float* lse, int* err, void* cuda_stream) {
   if (dtype != M3_KV_BF16 && dtype != M3_KV_F16) return set_error(M3_EINVAL, "dtype");
   if (n_seq < 0 || n_q < 0 || n_k < 0) return set_error(M3_EINVAL, "negative count");
   if (D != 64 && D != 128) return set_error(M3_EINVAL, "D: 64 or 128");
@@ -1231,6 +1231,7 @@ extern "C" int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, in
   a.o_token = o_token;
   a.o_head = o_head;
   a.lse = lse;
+  a.err = err;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.grp = Hq / Hkv;
@@ -1253,6 +1254,17 @@ extern "C" int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, in
   OPS_CK(launch_tc<false>(nt, D, f16, tq, tk, tv, a, (unsigned)(units * Hkv),
                           static_cast<cudaStream_t>(cuda_stream)));
   return M3_OK;
+}
+
+extern "C" int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int D,
+                              const void* q, int64_t q_token, int64_t q_head, const void* k,
+                              int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                              int64_t v_head, const int32_t* cu_q, const int32_t* cu_k,
+                              float scale, void* out, int64_t o_token, int64_t o_head, float* lse,
+                              void* cuda_stream) {
+  return attn_prompt(dtype, n_seq, n_q, n_k, Hq, Hkv, D, q, q_token, q_head, k, k_token, k_head, v,
+                     v_token, v_head, cu_q, cu_k, scale, out, o_token, o_head, lse, nullptr,
+                     cuda_stream);
 }
 
 extern "C" int64_t m3_attn_prefix_workspace(int n_rows, int Hq, int Hkv, int D, int prefix_pages,

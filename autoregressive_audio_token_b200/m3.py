@@ -27,7 +27,7 @@ M3_FAULT_NONE, M3_FAULT_ALLOC, M3_FAULT_H2D, M3_FAULT_GRAPH = 0, 1, 2, 3
 EXPORTED = ("m3_create", "m3_load_weights", "m3_load_depth_weights", "m3_kv_alloc", "m3_kv_set",
             "m3_kv_get", "m3_decode_frame", "m3_depth_decode", "m3_embed", "m3_quantize_int8",
             "m3_export_weight", "m3_frame_bytes", "m3_frame_kernels", "m3_depth_kernels", "m3_time_gemv", "m3_sample_noalloc", "m3_set_top_k",
-            "m3_load_feedback", "m3_generate", "m3_prefill", "m3_gumbel_fill", "m3_inject_fault",
+            "m3_load_feedback", "m3_generate", "m3_prefill", "m3_prefill_rows", "m3_gumbel_fill", "m3_inject_fault",
             "m3_stalled_wait", "m3_sync_status", "m3_last_error", "m3_destroy")
 
 
@@ -95,6 +95,7 @@ def load_library() -> C.CDLL:
     L.m3_sample_noalloc.argtypes = [vp, i32, vp, u64, u64, f32, f32, vp, vp]
     L.m3_load_feedback.argtypes = [vp, vp, C.POINTER(vp), i32]
     L.m3_prefill.argtypes = [vp, i32, i32, i32, vp, vp]
+    L.m3_prefill_rows.argtypes = [vp, i32, vp, vp, vp, vp]
     L.m3_generate.argtypes = [vp, i32, vp, u64, u64, vp, f32, f32, i32, vp, vp, vp]
     L.m3_gumbel_fill.argtypes = [u64, u64, u64, u64, i64, vp, vp]
     L.m3_inject_fault.argtypes = [vp, i32, i64]
@@ -320,6 +321,19 @@ def m3_prefill(ctx: int, row: int, start: int, x: torch.Tensor,
                h_last: torch.Tensor | None = None) -> None:
     """Prompt prefill of cache row `row` (see m3.h): x bf16 [n_tokens, H] on the GPU."""
     _check(lib.m3_prefill(ctx, row, start, x.shape[0], _ptr(x.contiguous()), _ptr(h_last)))
+
+
+def m3_prefill_rows(ctx: int, rows, n_tokens, x: torch.Tensor,
+                    h_last: torch.Tensor | None = None) -> None:
+    """Prompt prefill of several cache rows (see m3.h): x bf16 [sum of n_tokens, H] and
+    h_last bf16 [rows, H] on the GPU."""
+    n = len(rows)
+    r = (C.c_int32 * n)(*[int(v) for v in rows])
+    t = (C.c_int32 * n)(*[int(v) for v in n_tokens])
+    assert len(n_tokens) == n and x.shape[0] == sum(t), "x holds n_tokens' rows"
+    assert h_last is None or h_last.shape[0] == n, "h_last holds a row per prompt"
+    _check(lib.m3_prefill_rows(ctx, n, C.cast(r, C.c_void_p), C.cast(t, C.c_void_p),
+                               _ptr(x.contiguous()), _ptr(h_last)))
 
 
 def m3_gumbel_fill(seed: int, frame: int, row: int, index0: int, n: int,

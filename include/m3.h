@@ -204,6 +204,22 @@ M3_API int m3_kv_get(m3_ctx* ctx, int row, int n_positions, void* k_host, void* 
  * stream once. */
 M3_API int m3_prefill(m3_ctx* ctx, int row, int start, int n_tokens, const void* x, void* h_last);
 
+/* Prompt prefill of several cache rows at once: the prompts of a (cond,
+ * uncond) pair or of several songs, n_tokens[i] tokens for cache row rows[i],
+ * each from position 0, as m3_prefill does them one by one.  With bf16 weights
+ * on the GEMM path the prompts go through the layers packed, as many as fit
+ * the prefill chunk in one pass, so that the weights are read once for all of
+ * them; their attention is m3_attn_prompt (m3_ops.h), which rounds the softmax
+ * weights to bf16.  A prompt longer than the chunk, and every other weight
+ * type or shape, takes m3_prefill.
+ *  rows, n_tokens (HOST, [n_rows]): distinct rows; lengths from 1 to max_positions.
+ *  x (dev bf16 [sum of n_tokens, H]): the prompts' tokens, one prompt after another.
+ *  h_last (dev bf16 [n_rows, H], nullable): each prompt's last token's
+ *    final-normed hidden state.
+ * Allocates and synchronises as m3_prefill. */
+M3_API int m3_prefill_rows(m3_ctx* ctx, int n_rows, const int32_t* rows, const int32_t* n_tokens,
+                           const void* x, void* h_last);
+
 /* The end token.  With cfg.has_end_token the draw of m3_decode_frame chooses
  * among slice_len + 1 candidates: the code block and, as slice-relative code
  * slice_len, the end token (noise index end_token); the vocabulary mask of
