@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(384, 1)  // 168 registers, with one row tile (
 
 // --------------------------------------------------- a row's own positions --
 // One CTA: the (up to 16) query heads of one KV head of one row against a run
-// of its positions.  Each of 4 warps takes every 4th 16-position tile, K and
+// of its positions, or of the prefix's where that is short.  Each of 4 warps takes every 4th 16-position tile, K and
 // V by 16-byte asynchronous copies into its own ring, swizzled for ldmatrix;
 // S = Q K^T and O += P V on m16n8k16, fp32 softmax.  Positions past the length
 // and pages that are not there are filled with zeros, not read, and masked.
@@ -735,7 +735,9 @@ struct OwnArgs {
   int64_t ld_table;
   const int32_t* lens;
   int n_pages, shift, max_pages;
-  int n_rows, Hq, Hkv, grp, mtiles, splits;
+  const int32_t* prefix_pages;  // pre_splits > 0: the prefix, read by every row for itself
+  int prefix_len, pre_splits;
+  int n_rows, Hq, Hkv, grp, mtiles, splits;  // splits: of the prefix, then of the own positions
   float c;
   float* part_o;    // [splits][n_rows * Hq][D]
   float2* part_ml;  // [splits][n_rows * Hq]
@@ -760,10 +762,14 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   const int mt = x % a.mtiles;
   x /= a.mtiles;
   const int g = x % a.Hkv, b = x / a.Hkv;
-  const int len = (int)min((long long)max(a.lens[b], 0), (long long)a.max_pages << a.shift);
+  const bool pre = split < a.pre_splits;
+  const int len = pre ? a.prefix_len
+                      : (int)min((long long)max(a.lens[b], 0), (long long)a.max_pages << a.shift);
   const int tiles = (len + kOwnTile - 1) / kOwnTile;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int t0 = min(tiles, split * per), t1 = min(tiles, t0 + per);
+  const int of = pre ? a.pre_splits : a.splits - a.pre_splits;
+  const int per = (tiles + of - 1) / of;
+  const int t0 = min(tiles, (pre ? split : split - a.pre_splits) * per);
+  const int t1 = min(tiles, t0 + per);
   const size_t rows = (size_t)a.n_rows * a.Hq;
   const int heads = min(16, a.grp - mt * 16);
   const size_t id0 = (size_t)split * rows + (size_t)b * a.Hq + g * a.grp + mt * 16;
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   uint8_t* ring = own_raw + (size_t)warp * kOwnStages * 2 * kOwnTile * ROWB;
   const uint32_t ring_u = smem_u32(ring);
   const int nmine = t1 - t0 > warp ? (t1 - t0 - warp + kOwnWarps - 1) / kOwnWarps : 0;
-  const int32_t* trow = a.table + (size_t)b * a.ld_table;
+  const int32_t* trow = pre ? a.prefix_pages : a.table + (size_t)b * a.ld_table;
   const size_t page_elems = (size_t)2 * a.Hkv * D << a.shift;
   // the page numbers of this warp's tiles, 32 tiles at a time (one per lane)
   int held = -1;
@@ -951,8 +957,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
 }
 
 // ------------------------------------------------------------------ join ---
-// One CTA per (row, query head): the parts' (max, sum, unnormalised o).  Its
-// D / 4 lanes a part, the parts side by side, then one sum over those.
+// A row and query head: the parts' (max, sum, unnormalised o), D / 4 lanes a
+// part, the parts side by side, then one sum over those.
 struct JoinArgs {
   const float* part_o;
   const float2* part_ml;
@@ -966,54 +972,57 @@ struct JoinArgs {
 constexpr int kJoinThreads = 128;
 constexpr int kMaxParts = 256;
 
-template <int D, int F16>
+// WARPS per (row, query head): 4, or 1 where there are rows enough.
+template <int D, int F16, int WARPS>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const JoinArgs a) {
-  constexpr int W = D / 4, SIDE = kJoinThreads / W;  // lanes per part, parts side by side
-  __shared__ float f[kMaxParts];
+  constexpr int T = 32 * WARPS, ROWS = kJoinThreads / T;  // threads per row, rows per CTA
+  constexpr int W = D / 4, SIDE = T / W;                  // lanes per part, parts side by side
+  __shared__ float f[ROWS][kMaxParts];
   __shared__ float red[2][kJoinThreads / 32];
-  __shared__ float4 acc[SIDE][W];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const size_t id = blockIdx.x, rows = (size_t)a.n_rows * a.Hq;
+  __shared__ float4 acc[ROWS][SIDE][W];
+  const int tid = threadIdx.x % T, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = threadIdx.x / T;
+  auto sync = [&]() {
+    if constexpr (WARPS == 1) __syncwarp();
+    else __syncthreads();
+  };
+  const size_t rows = (size_t)a.n_rows * a.Hq, id = (size_t)blockIdx.x * ROWS + r;
   pdl_wait();
+  if (id >= rows) return;
+  const int b = (int)(id / a.Hq), h = (int)(id % a.Hq);
   if (a.lens[b] < 0) return;  // padding
   float m = -INFINITY;
-  float2 ml[kMaxParts / kJoinThreads];
-#pragma unroll
-  for (int i = 0; i < kMaxParts / kJoinThreads; ++i) {
-    const int p = tid + i * kJoinThreads;
-    ml[i] = p < a.parts ? __ldcg(a.part_ml + p * rows + id) : make_float2(-INFINITY, 0.0f);
-    m = fmaxf(m, ml[i].x);
-  }
+  for (int p = tid; p < a.parts; p += T) m = fmaxf(m, __ldcg(a.part_ml + p * rows + id).x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  if (lane == 0) red[0][warp] = m;
-  __syncthreads();
+  if constexpr (WARPS > 1) {
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, red[0][k]);
+    for (int k = 0; k < WARPS; ++k) m = fmaxf(m, red[0][k]);
+  }
   float l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kMaxParts / kJoinThreads; ++i) {
-    const int p = tid + i * kJoinThreads;
-    if (p < a.parts) {
-      // a part without a key has no o
-      const float x = ml[i].x == -INFINITY && ml[i].y == 0.0f ? 0.0f : ex2(ml[i].x - m);
-      f[p] = x;
-      if (x != 0.0f) l += ml[i].y * x;
-    }
+  for (int p = tid; p < a.parts; p += T) {
+    const float2 ml = __ldcg(a.part_ml + p * rows + id);
+    // a part without a key has no o
+    const float x = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ex2(ml.x - m);
+    f[r][p] = x;
+    if (x != 0.0f) l += ml.y * x;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
-  l = 0.0f;
+  if (WARPS > 1 && lane == 0) red[1][warp] = l;
+  sync();
+  if constexpr (WARPS > 1) {
+    l = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) l += red[1][k];
+    for (int k = 0; k < WARPS; ++k) l += red[1][k];
+  }
   const int side = tid / W, d = (tid % W) * 4;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
   for (int p = side; p < a.parts; p += SIDE) {
-    const float x = f[p];
+    const float x = f[r][p];
     if (x == 0.0f) continue;
     const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (p * rows + id) * D + d));
     y.x += v.x * x;
@@ -1021,12 +1030,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const JoinArgs 
     y.z += v.z * x;
     y.w += v.w * x;
   }
-  acc[side][tid % W] = y;
-  __syncthreads();
+  if constexpr (SIDE > 1) {
+    acc[r][side][tid % W] = y;
+    sync();
+  }
   if (tid < W) {
 #pragma unroll
     for (int k = 1; k < SIDE; ++k) {
-      const float4 v = acc[k][tid];
+      const float4 v = acc[r][k][tid];
       y.x += v.x;
       y.y += v.y;
       y.z += v.z;
@@ -1132,13 +1143,22 @@ cudaError_t launch_own_t(const OwnArgs& a, const JoinArgs& j, bool after_prefix,
                     after_prefix, a);
     if (e != cudaSuccess) return e;
   }
-  return launch_ex(attn_join_kernel<D, F16>, dim3((unsigned)(j.n_rows * j.Hq)), dim3(kJoinThreads),
-                   0, st, after_prefix || a.splits > 0, j);
+  // a warp per row and head once four would be more than 16 CTAs per SM
+  const long long rows = (long long)j.n_rows * j.Hq;
+  const bool pdl = after_prefix || a.splits > 0;
+  if (rows > 16ll * sm_count())
+    return launch_ex(attn_join_kernel<D, F16, 1>, dim3((unsigned)((rows + 3) / 4)),
+                     dim3(kJoinThreads), 0, st, pdl, j);
+  return launch_ex(attn_join_kernel<D, F16, 4>, dim3((unsigned)rows), dim3(kJoinThreads), 0, st,
+                   pdl, j);
 }
+
+constexpr long long kAlonePositions = 2048;  // rows x prefix, see plan_prefix
 
 // How m3_attn_prefix splits its work; the workspace follows from it.
 struct PrefixPlan {
   int grp = 0, tpt = 0, nt = 0, units = 0;  // rows per row tile, row tiles of a CTA, such groups
+  bool alone = false;                       // the prefix is read by every row for itself
   int pre_splits = 0, pre_tiles = 0;     // splits of the prefix, key tiles of each
   int mtiles = 0, own_splits = 0;
   int64_t rows = 0, bytes = 0;
@@ -1155,11 +1175,30 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
   const int nsm = sm_count();
   p->grp = Hq / Hkv;
   p->tpt = kTile / p->grp;
-  p->nt = n_rows > p->tpt ? 2 : 1;
+  // Two row tiles per CTA from four pairs on (256 rows of 4 heads a KV head,
+  // prefix 9000: 79.9 against 86.6 us with one; 1024 rows: 260 against 320).
+  // Below, CTAs of one tile leave room for the rows' own positions beside them
+  // (128 rows: 49.7 against 50.2)
+  p->nt = n_rows >= 8 * p->tpt ? 2 : 1;
   p->units = (n_rows + p->nt * p->tpt - 1) / (p->nt * p->tpt);
   p->rows = (int64_t)n_rows * Hq;
+  p->mtiles = (p->grp + 15) / 16;
   const long long key_tiles = (prefix + kTile - 1) / kTile;
-  if (key_tiles > 0) {
+  const long long ctas = (long long)n_rows * Hkv * p->mtiles;
+  // splits into runs of 64 positions at least, for about four CTAs per SM
+  auto small_splits = [&](long long positions, long long all) {
+    long long s = (4ll * nsm * positions + all * ctas - 1) / (all * ctas);
+    const long long most = (positions + 63) / 64;
+    s = s > most ? most : s;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  };
+  // A short prefix, or one row: every row reads it for itself, in one launch with
+  // its own positions (4 rows x 300: 6.7 against 9.7 us; 16 x 300: 13.1 against
+  // 11.2; 2 x 4500: 15.2 against 13.4)
+  p->alone = key_tiles > 0 && (n_rows == 1 || n_rows * prefix <= kAlonePositions);
+  if (p->alone) {
+    p->pre_splits = small_splits(prefix, prefix + own);
+  } else if (key_tiles > 0) {
     // one round of CTAs over the SMs (a CTA fills one), whole key tiles
     long long s = nsm / ((long long)p->units * Hkv);
     s = s < 1 ? 1 : s > key_tiles ? key_tiles : s;
@@ -1167,19 +1206,12 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
     p->pre_tiles = (int)((key_tiles + s - 1) / s);
     p->pre_splits = (int)((key_tiles + p->pre_tiles - 1) / p->pre_tiles);
   }
-  p->mtiles = (p->grp + 15) / 16;
-  if (own > 0) {
-    // about four CTAs per SM, of 64 positions at least
-    const long long ctas = (long long)n_rows * Hkv * p->mtiles;
-    long long s = (4ll * nsm + ctas - 1) / ctas, most = (own + 63) / 64;
-    s = s > most ? most : s;
-    p->own_splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-  }
+  if (own > 0) p->own_splits = small_splits(own, p->alone ? prefix + own : own);
   const int64_t parts = p->pre_splits + p->own_splits;
   p->bytes = ((parts * p->rows * 8 + 15) & ~(int64_t)15) + parts * p->rows * D * 4;
   if (p->bytes == 0) p->bytes = 16;
   return p->rows <= INT_MAX && (long long)p->units * Hkv * p->pre_splits <= INT_MAX &&
-         (long long)n_rows * Hkv * p->mtiles * p->own_splits <= INT_MAX;
+         ctas * (p->own_splits + (p->alone ? p->pre_splits : 0)) <= INT_MAX;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -1309,11 +1341,12 @@ extern "C" int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, con
   // pages without a pool hold nothing
   if (n_pages == 0) prefix_len = 0;
   const int pre = prefix_len > 0 ? p.pre_splits : 0, own = n_pages > 0 ? p.own_splits : 0;
+  const bool shared = pre > 0 && !p.alone;
   const int64_t parts = pre + own;
   float2* ml = static_cast<float2*>(workspace);
   float* po = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        ((parts * p.rows * 8 + 15) & ~(int64_t)15));
-  if (pre > 0) {
+  if (shared) {
     AttnTcArgs a{};
     a.pages = prefix_pages;
     a.n_prefix_pages = n_prefix_pages;
@@ -1357,15 +1390,18 @@ extern "C" int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, con
   o.Hkv = Hkv;
   o.grp = p.grp;
   o.mtiles = p.mtiles;
-  o.splits = own;
+  o.prefix_pages = prefix_pages;
+  o.prefix_len = prefix_len;
+  o.pre_splits = shared ? 0 : pre;
+  o.splits = own + o.pre_splits;
   o.c = scale * kLog2e;
-  o.part_o = po + (int64_t)pre * p.rows * D;
-  o.part_ml = ml + (int64_t)pre * p.rows;
+  o.part_o = po + (int64_t)(pre - o.pre_splits) * p.rows * D;
+  o.part_ml = ml + (int64_t)(pre - o.pre_splits) * p.rows;
   JoinArgs j{po, ml, lens, static_cast<uint16_t*>(out), o_row, o_head, lse, n_rows, Hq, (int)parts};
   if (D == 128)
-    OPS_CK(f16 ? (launch_own_t<128, 1>(o, j, pre > 0, st)) : (launch_own_t<128, 0>(o, j, pre > 0, st)));
+    OPS_CK(f16 ? (launch_own_t<128, 1>(o, j, shared, st)) : (launch_own_t<128, 0>(o, j, shared, st)));
   else
-    OPS_CK(f16 ? (launch_own_t<64, 1>(o, j, pre > 0, st)) : (launch_own_t<64, 0>(o, j, pre > 0, st)));
+    OPS_CK(f16 ? (launch_own_t<64, 1>(o, j, shared, st)) : (launch_own_t<64, 0>(o, j, shared, st)));
   return M3_OK;
 }
 

@@ -99,7 +99,7 @@ M3_API int64_t m3_attn_prefix_workspace(int n_rows, int Hq, int Hkv, int D, int 
 
 /* One-token attention of n_rows rows that share a prefix: row b attends to
  * positions 0..prefix_len - 1 in the pages prefix_pages[], read once for the
- * whole batch, and to its own lens[b] positions in the pages of its table
+ * whole batch (where it is short, by each row), and to its own lens[b] positions in the pages of its table
  * row.  q, out [n_rows][Hq][D] with strides, lse as in m3_attn_prompt.
  * lens[b] < 0 marks a row of padding: its out and lse stay as they are.  A row
  * with nothing to attend to gets out = 0 and lse = -inf.  lens[b] past

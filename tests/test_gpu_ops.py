@@ -309,7 +309,8 @@ def check_prefix(out, lse, q, shared, own, lens, scale, dtype):
 
 
 PREFIXES = [(1, 0, [0]), (1, 1, [0]), (1, 0, [1]), (2, 300, [5, 40]), (3, 128, [0, 128, 17]), (4, 129, [-1, 3, 0, 250]),
-            (5, 1000, [16, 15, 17, 700, 1]), (40, 2000, [7 * i % 300 for i in range(40)]), (3, 0, [0, 33, -1])]
+            (5, 1000, [16, 15, 17, 700, 1]), (40, 2000, [7 * i % 300 for i in range(40)]), (3, 0, [0, 33, -1]),
+            (1, 2500, [70]), (2, 1100, [0, 9]), (140, 1100, [i % 37 - 1 for i in range(140)])]
 
 
 @pytest.mark.parametrize("hq,hk,d,page,dtype", [(8, 2, 128, 16, BF16), (4, 4, 64, 256, F16), (6, 1, 64, 32, BF16),
