@@ -7,6 +7,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "m3_ops.h"
 #include "ops.cuh"
 
@@ -283,6 +284,7 @@ struct RuleArgs {
   const uint32_t* mask;
   const int32_t* mask_row;
   int vocab, n_history, n_bias, n_masks, words, run, runs;
+  int parts, range, slots;  // of logit_touch_kernel
 };
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
@@ -471,8 +473,226 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
   }
 }
 
+// The same in two launches, for logits that fill the GPU several times over:
+// there the waits of a run's history, between its loads and its stores, leave
+// HBM idle (192 x 200000, fp32: 95 us in one launch, 79 in two; 64 x 200000: 34
+// and 32; 64 x 50000: 13.5 and 17.5).  The first streams the logits under the mask alone, with nothing to wait for; the
+// second takes up a row's noted tokens, kept in a hash table in shared memory
+// that it builds while the first one ends.
+constexpr int kMaskThreads = 256;
+constexpr int kMaskPieces = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(kMaskThreads) logit_mask_kernel(const RuleArgs a) {
+  constexpr int VEC = 16 / sizeof(T);
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, row = blockIdx.x / a.runs, part = blockIdx.x % a.runs;
+  const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
+  T* out = static_cast<T*>(a.out) + row * a.ld_out;
+  const uint32_t* mask = nullptr;
+  if (a.mask) {
+    const int m = a.mask_row ? __ldg(a.mask_row + row) : (a.n_masks == 1 ? 0 : row);
+    if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * a.words;
+  }
+  if (!mask && in == out) return;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(in) / sizeof(T)) % VEC);
+  const bool vec_out = (reinterpret_cast<uintptr_t>(out) / sizeof(T)) % VEC == (unsigned)lead;
+  const long long s0 = (long long)part * a.run - lead;
+  const int lo = (int)max(s0, 0ll), hi = (int)min(s0 + a.run, (long long)a.vocab);
+  uint4 raw[kMaskPieces];
+  uint32_t word[kMaskPieces];
+#pragma unroll
+  for (int u = 0; u < kMaskPieces; ++u) {
+    const long long i0 = s0 + (u * kMaskThreads + tid) * VEC;
+    const bool whole = i0 >= lo && i0 + VEC <= hi;
+    if (whole) raw[u] = *reinterpret_cast<const uint4*>(in + i0);
+    word[u] = mask && whole ? __ldg(mask + (i0 >> 5)) : ~0u;
+  }
+#pragma unroll
+  for (int u = 0; u < kMaskPieces; ++u) {
+    const long long i0 = s0 + (u * kMaskThreads + tid) * VEC;
+    if (i0 < lo || i0 + VEC > hi) continue;
+    T x[VEC];
+    *reinterpret_cast<uint4*>(x) = raw[u];
+    if (mask) {
+      const int sh = (int)(i0 & 31);
+      const uint32_t w1 = sh + VEC > 32 ? __ldg(mask + (i0 >> 5) + 1) : 0u;
+      const uint32_t bits = __funnelshift_r(word[u], w1, sh);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q)
+        if (!((bits >> q) & 1)) x[q] = from_f<T>(-INFINITY);
+    }
+    if (vec_out) {
+      *reinterpret_cast<uint4*>(out + i0) = *reinterpret_cast<const uint4*>(x);
+    } else {
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) out[i0 + q] = x[q];
+    }
+  }
+  // the run's first and last few, where a 16-byte piece reaches past it
+  const int head = (int)min((long long)hi, s0 + (lo - s0 + VEC - 1) / VEC * VEC);
+  const int tail = (int)max((long long)head, s0 + (hi - s0) / VEC * VEC);
+  if (tid < (head - lo) + (hi - tail)) {
+    const int at = tid < head - lo ? lo + tid : tail + (tid - (head - lo));
+    out[at] = !mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1) ? in[at]
+                                                                   : from_f<T>(-INFINITY);
+  }
+}
+
+constexpr int kTouchSlots = 16384;   // of the largest table
+constexpr int kTouchTokens = 8192;   // it takes up to this many different tokens
+
+inline size_t touch_smem(int slots, bool biases) {
+  return (size_t)slots * (biases ? 12 : 8) + (size_t)kTouchTokens * 2;
+}
+
+constexpr int kTouchThreads = 1024;
+constexpr int kAtOnce = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleArgs a) {
+  extern __shared__ int touch_raw[];
+  const int S = a.slots;
+  int* key = touch_raw;       // [S] token, or -1
+  int* cnt = key + S;         // [S] times in the history
+  int* code = cnt + S;        // [S] n_bias - its first bias entry, or 0 (with biases)
+  const bool biases = a.n_bias > 0;
+  uint16_t* list = reinterpret_cast<uint16_t*>(touch_raw + S * (biases ? 3 : 2));
+  __shared__ int n_list, twice;
+  const int tid = threadIdx.x, row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int lo = part * a.range, hi = min(a.vocab, lo + a.range);
+  const unsigned span = (unsigned)max(hi - lo, 0);
+  const int shift = __clz(S - 1);
+  for (int i = tid; i < S; i += kTouchThreads) {
+    key[i] = -1;
+    cnt[i] = 0;
+    if (biases) code[i] = 0;
+  }
+  if (tid == 0) n_list = twice = 0;
+  __syncthreads();
+  auto slot_of = [&](int id) -> int {
+    int h = (int)(((unsigned)id * 2654435761u) >> shift);  // multiplicative hashing (Knuth)
+    for (;;) {  // ends: the tokens are fewer than the slots
+      const int was = atomicCAS(&key[h], -1, id);
+      if (was == -1 || was == id) return h;
+      h = (h + 1) & (S - 1);
+    }
+  };
+  const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
+  const float* val = a.bias + (size_t)row * a.n_bias;
+  if (a.history) {
+    const int32_t* hist = a.history + row * a.ld_history;
+    int n = a.n_history;
+    if (a.hist_len) n = min(n, max(0, __ldg(a.hist_len + row)));
+    for (int i0 = tid; i0 < n; i0 += kAtOnce * kTouchThreads) {  // several loads under way
+      int id[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        id[u] = i0 + u * kTouchThreads < n ? __ldg(hist + i0 + u * kTouchThreads) : -1;
+#pragma unroll 1
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int v = u == 0 ? id[0] : u == 1 ? id[1] : u == 2 ? id[2] : id[3];
+        if ((unsigned)v - (unsigned)lo < span) atomicAdd(&cnt[slot_of(v)], 1);
+      }
+    }
+  }
+  // the first entry of each token owns it, whatever the order of the atomics
+  for (int e = tid; e < a.n_bias; e += kTouchThreads) {
+    const int id = __ldg(ids + e);
+    if ((unsigned)id - (unsigned)lo < span) atomicMax(&code[slot_of(id)], a.n_bias - e);
+  }
+  __syncthreads();
+  if (biases) {
+    bool again = false;
+    for (int e = tid; e < a.n_bias; e += kTouchThreads) {
+      const int id = __ldg(ids + e);
+      if ((unsigned)id - (unsigned)lo < span) again |= code[slot_of(id)] != a.n_bias - e;
+    }
+    if (again) twice = 1;
+    __syncthreads();
+  }
+  // the taken slots side by side (one counter for every token would take the
+  // tokens one by one)
+  for (int i = tid; i < S; i += kTouchThreads) {
+    const unsigned taken = __ballot_sync(~0u, key[i] >= 0);
+    int base = 0;
+    if ((tid & 31) == 0 && taken) base = smem_add(&n_list, __popc(taken));
+    base = __shfl_sync(~0u, base, 0);
+    if ((taken >> (tid & 31)) & 1)
+      list[base + __popc(taken & ((1u << (tid & 31)) - 1))] = (uint16_t)i;
+  }
+  const float rep = a.rep ? __ldg(a.rep + row) : 1.0f, freq = a.freq ? __ldg(a.freq + row) : 0.0f;
+  const float pres = a.pres ? __ldg(a.pres + row) : 0.0f, inv = 1.0f / rep;
+  const uint32_t* mask = nullptr;
+  if (a.mask) {
+    const int m = a.mask_row ? __ldg(a.mask_row + row) : (a.n_masks == 1 ? 0 : row);
+    if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * a.words;
+  }
+  T* out = static_cast<T*>(a.out) + row * a.ld_out;
+  __syncthreads();
+  pdl_wait();  // the logits are there
+  for (int k0 = tid; k0 < n_list; k0 += kAtOnce * kTouchThreads) {
+    int h[kAtOnce];
+    float y[kAtOnce];
+    bool ok[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int k = k0 + u * kTouchThreads;
+      h[u] = list[min(k, n_list - 1)];
+      const int at = key[h[u]];
+      ok[u] = k < n_list && (!mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1));
+      y[u] = to_f(__ldcg(out + at));
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int at = key[h[u]], c = cnt[h[u]];
+      float x = y[u];
+      if (c > 0) {
+        x = x > 0.0f ? x * inv : x * rep;
+        x -= freq * (float)c;
+        x -= pres;
+      }
+      if (ok[u] && biases && code[h[u]] > 0) {
+        const int e = a.n_bias - code[h[u]];
+        float b = __ldg(val + e);
+        if (twice)  // some token has several entries: added up in their order
+          for (int f = e + 1; f < a.n_bias; ++f)
+            if (__ldg(ids + f) == at) b += __ldg(val + f);
+        x += b;
+      }
+      if (ok[u]) out[at] = from_f<T>(x);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_rules_two(RuleArgs a, int n_rows, bool stream_out, cudaStream_t st) {
+  if (stream_out) {
+    a.run = kMaskThreads * kMaskPieces * (16 / (int)sizeof(T));
+    a.runs = (int)(((long long)a.vocab + 7 + a.run - 1) / a.run);
+    logit_mask_kernel<T><<<(unsigned)(n_rows * a.runs), kMaskThreads, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!a.history && !a.n_bias)) return e;
+  }
+  // a row's tokens in one table, or each table a part of the vocabulary
+  const long long tokens = (long long)a.n_history + a.n_bias;
+  a.parts = tokens <= kTouchTokens ? 1 : (a.vocab + kTouchTokens - 1) / kTouchTokens;
+  a.range = (a.vocab + a.parts - 1) / a.parts;
+  const long long most = tokens < a.range ? tokens : a.range;
+  a.slots = 256;  // a quarter of the slots or more stays free
+  while (a.slots * 3ll < most * 4) a.slots <<= 1;
+  const size_t smem = touch_smem(a.slots, a.n_bias > 0);
+  const cudaError_t e =
+      cudaFuncSetAttribute(logit_touch_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)touch_smem(kTouchSlots, true));
+  if (e != cudaSuccess) return e;
+  return launch_ex(logit_touch_kernel<T>, dim3((unsigned)(n_rows * a.parts)), dim3(kTouchThreads),
+                   smem, st, stream_out, a);
+}
+
 template <typename T>
 cudaError_t launch_rules(const RuleArgs& a, int n_rows, cudaStream_t st) {
+  if (a.parts) return launch_rules_two<T>(a, n_rows, a.in != a.out || a.mask, st);
   const size_t smem =
       a.history || a.n_bias ? 6 * (size_t)a.run + 16 * (size_t)a.n_bias : 0;
   if (smem > 40 * 1024) {  // past the default limit with what the kernel holds itself
@@ -638,6 +858,12 @@ extern "C" int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logi
     a.run >>= 1;
   a.runs = (int)(((long long)vocab + 7 + a.run - 1) / a.run);
   if ((long long)a.runs * n_rows > INT_MAX) return set_error(M3_EINVAL, "too many rows");
+  if (same && !mask && !a.history && !n_bias) return M3_OK;
+  // two launches from twelve runs of the longest per SM on, and where penalties or
+  // biases alone touch logits in place
+  if ((a.history || n_bias) &&
+      ((same && !mask) || (long long)a.runs * n_rows >= 12ll * sm_count() * (kRuleRun / a.run)))
+    a.parts = 1;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (dtype == M3_LOGITS_F32) OPS_CK(launch_rules<float>(a, n_rows, st));
   else if (dtype == M3_LOGITS_BF16) OPS_CK(launch_rules<__nv_bfloat16>(a, n_rows, st));

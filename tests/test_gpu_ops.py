@@ -397,7 +397,9 @@ def rule_inputs(r, n, nh, nb, nm, seed):
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("r,n,nh,nb,nm", [(1, 1, 1, 1, 1), (2, 16385, 1500, 16, 1), (3, 31, 9, 40, 2), (5, 1000, 0, 7, 0),
                                           (4, 4097, 70, 0, 3), (700, 8191, 33, 5, 4), (300, 20000, 50, 0, 0),
-                                          (300, 20000, 0, 9, 0), (300, 20001, 0, 0, 2), (2, 50001, 4096, 300, 2)])
+                                          (300, 20000, 0, 9, 0), (300, 20001, 0, 0, 2),
+                                          (120, 130001, 600, 40, 3), (110, 140000, 9000, 300, 1),  # two launches
+                                          (2, 50001, 4096, 300, 2)])
 def test_rules(ops, r, n, nh, nb, nm, dtype):
     x = (4 * torch.randn(r, n, generator=gen(n), device="cuda")).to(dtype)
     history, hist_len, rep, freq, pres, ids, bias, mask, row = rule_inputs(r, n, nh, nb, nm, n + r)
@@ -407,6 +409,9 @@ def test_rules(ops, r, n, nh, nb, nm, dtype):
     y = x.clone()
     ops.m3_logit_rules(y, y, history, hist_len, rep, freq, pres, ids, bias, mask, row)
     assert torch.equal(y, out)
+    y = x.clone()  # in place without a mask: only the named tokens are touched
+    ops.m3_logit_rules(y, y, history, hist_len, rep, freq, pres, ids, bias)
+    check_rules(y, x, history, hist_len, rep, freq, pres, ids, bias, None, None)
 
 
 @pytest.mark.parametrize("dtype", [F32, F16])
