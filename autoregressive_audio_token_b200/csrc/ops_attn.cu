@@ -794,24 +794,39 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
     return __shfl_sync(~0u, held, i & 31);
   };
   uint32_t live = 0;  // bit (i % 32): tile i has its page
+  // a lane's 16-byte pieces: row lr + RPP e, piece lc, e < PPL; the swizzle
+  // piece ^ (row & 7) takes its lane and its e apart
+  constexpr int RPP = 32 / CH, PPL = kOwnTile / RPP;
+  const int lr = lane / CH, lc = lane % CH;
+  const uint32_t lane_src = lr * D + lc * 8, lane_dst = lr * ROWB;
+  const uint32_t lane_piece = lc ^ (lr & 7);
   auto fetch = [&](int i) {
     if (i < nmine) {
       const int t = t0 + warp + i * kOwnWarps;
       const int page = page_of(i);
       live = page >= 0 ? live | (1u << (i & 31)) : live & ~(1u << (i & 31));
       const int p0 = t * kOwnTile, off = p0 & ((1 << a.shift) - 1);
-      const int nv = page >= 0 ? min(kOwnTile, len - p0) : 0;
       const uint16_t* kp = a.pool + (size_t)max(page, 0) * page_elems +
-                           (((size_t)g << a.shift) + off) * D;
+                           (((size_t)g << a.shift) + off) * D + lane_src;
       const uint16_t* vp = kp + ((size_t)a.Hkv << a.shift) * D;
-      const uint32_t dst = ring_u + (i % kOwnStages) * 2 * kOwnTile * ROWB;
+      const uint32_t dst = ring_u + (i % kOwnStages) * 2 * kOwnTile * ROWB + lane_dst;
+      const int nv = page >= 0 ? len - p0 : 0;  // rows of the tile that are there
+      if (nv >= kOwnTile) {
 #pragma unroll
-      for (int e = 0; e < kOwnTile * CH / 32; ++e) {
-        const int r = (e * 32 + lane) / CH, ch = (e * 32 + lane) % CH;
-        const uint32_t o = r * ROWB + ((ch ^ (r & 7)) << 4);
-        const int rs = r < nv ? r : 0;
-        cp16(dst + o, kp + rs * D + ch * 8, r < nv);
-        cp16(dst + kOwnTile * ROWB + o, vp + rs * D + ch * 8, r < nv);
+        for (int e = 0; e < PPL; ++e) {
+          const uint32_t o = e * RPP * ROWB + ((lane_piece ^ ((e * RPP) & 7)) << 4);
+          cp16(dst + o, kp + e * RPP * D, true);
+          cp16(dst + kOwnTile * ROWB + o, vp + e * RPP * D, true);
+        }
+      } else {  // zeros past them, and nothing read
+#pragma unroll
+        for (int e = 0; e < PPL; ++e) {
+          const uint32_t o = e * RPP * ROWB + ((lane_piece ^ ((e * RPP) & 7)) << 4);
+          const bool there = lr + e * RPP < nv;
+          const int back = there ? e * RPP * D : -(int)lane_src;
+          cp16(dst + o, kp + back, there);
+          cp16(dst + kOwnTile * ROWB + o, vp + back, there);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -858,34 +873,33 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
         mma16816<F16>(s[j], qa[kk + 1][0], qa[kk + 1][1], qa[kk + 1][2], qa[kk + 1][3], b2, b3);
       }
     }
-    float mx[2] = {-INFINITY, -INFINITY};
+    if (nv < kOwnTile) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[j][e] = 8 * j + 2 * tig + (e & 1) < nv ? s[j][e] * a.c : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[j][e]);
-      }
-    float f[2];
+        for (int e = 0; e < 4; ++e)
+          if (8 * j + 2 * tig + (e & 1) >= nv) s[j][e] = -INFINITY;
+    }
+    // the reference maximum is raised only past 2^kRaise, as in attn_tc_kernel
+    float f[2] = {1.0f, 1.0f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 1));
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 2));
-      const float mn = fmaxf(m[h], mx[h]);
-      f[h] = mn == -INFINITY ? 1.0f : ex2(m[h] - mn);
-      m[h] = mn;
+      float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])) * a.c;
+      x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+      if (x - m[h] > kRaise || (m[h] == -INFINITY && x > m[h])) {
+        f[h] = ex2(m[h] - x);
+        m[h] = x;
+      }
     }
     const float r0 = m[0] == -INFINITY ? 0.0f : m[0], r1 = m[1] == -INFINITY ? 0.0f : m[1];
-    float ls[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[j][e] = ex2(s[j][e] - ((e >> 1) ? r1 : r0));
-        ls[e >> 1] += s[j][e];
-      }
-    l[0] = l[0] * f[0] + ls[0];  // this lane's share of the row's sum
-    l[1] = l[1] * f[1] + ls[1];
+      for (int e = 0; e < 4; ++e) s[j][e] = ex2(fmaf(s[j][e], a.c, (e >> 1) ? -r1 : -r0));
+    // this lane's share of the rows' sums
+    l[0] = l[0] * f[0] + ((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]));
+    l[1] = l[1] * f[1] + ((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]));
     if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) {
 #pragma unroll
       for (int j = 0; j < NTO; ++j) {
