@@ -1567,11 +1567,11 @@ extern "C" int m3_prefill_rows(m3_ctx* c, int n_rows, const int32_t* rows,
     if (!c->loaded[l]) return fail(M3_ESTATE, "layer " + std::to_string(l) + " not loaded");
   if (h_last && !c->final_norm) return fail(M3_ESTATE, "final norm not loaded");
   if (n_rows < 1 || n_rows > c->kv_rows) return fail(M3_EINVAL, "n_rows out of 1..cache rows");
-  std::vector<char> seen(c->kv_rows, 0);
   int longest = 0;
   for (int i = 0; i < n_rows; ++i) {
-    if (rows[i] < 0 || rows[i] >= c->kv_rows || seen[rows[i]]) return fail(M3_EINVAL, "rows");
-    seen[rows[i]] = 1;
+    if (rows[i] < 0 || rows[i] >= c->kv_rows) return fail(M3_EINVAL, "rows");
+    for (int k = 0; k < i; ++k)
+      if (rows[k] == rows[i]) return fail(M3_EINVAL, "a row twice");
     if (n_tokens[i] < 1) return fail(M3_EINVAL, "n_tokens");
     if (n_tokens[i] > c->kv_max_pos) return fail(M3_ECAPACITY, "n_tokens outside the KV capacity");
     longest = n_tokens[i] > longest ? n_tokens[i] : longest;

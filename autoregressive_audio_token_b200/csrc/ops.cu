@@ -751,6 +751,10 @@ extern "C" int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
       (n_tokens && (!positions || !slots || !seqs)))
     return set_error(M3_EINVAL, "null argument");
   if (free_at == taken) return set_error(M3_EINVAL, "free_at and taken are the same word");
+  // every CTA reads the lengths while one writes the sums
+  for (const int32_t* in : {fresh, cached})
+    if (in && ((lens < in + n_req && in < lens + n_req) || (cu < in + n_req && in < cu + n_req + 1)))
+      return set_error(M3_EINVAL, "cu or lens overlaps fresh or cached");
   if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots) |
        reinterpret_cast<uintptr_t>(seqs)) & 15)
     return set_error(M3_EINVAL, "positions, slots and seqs have to be 16-byte aligned");

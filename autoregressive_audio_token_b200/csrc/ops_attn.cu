@@ -84,6 +84,8 @@ struct AttnTcArgs {
   uint16_t* out;
   int64_t o_token, o_head;
   float* lse;
+  const uint16_t *q, *k, *v;  // as the tensor maps have them (see kept_apart)
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
   // shared prefix
   const int32_t* pages;
   int n_prefix_pages, n_pages, shift, prefix_len, n_rows, splits, tiles_per_split;
@@ -275,6 +277,71 @@ __device__ __forceinline__ bool find_prompt_work(const AttnTcArgs& a, int w, int
     before += all;
   }
   return false;
+}
+
+// Values of keys that a row does not attend to come to it through 0 * v in the
+// key tile on the diagonal, which is not 0 for an infinity or a NaN.  For 32
+// columns of o that hold one: if such a key is where it came from, the row is
+// summed again over its own keys alone, with the same m, one by one.  Slow, and
+// reached by such values only.
+template <int D, int F16>
+__device__ __forceinline__ void kept_apart(const AttnTcArgs& a, int h, int head, int at, int key0,
+                                           int keys, int end, int col, float mc, uint32_t* o) {
+  constexpr uint32_t kMask = F16 ? 0x7C00u : 0x7F80u;  // an exponent of ones: no number
+  const uint16_t* v = a.v + (int64_t)key0 * a.v_token + (int64_t)h * a.v_head + col;
+  bool strange = false;
+  for (int j = max(keys, 0); j < end && !strange; ++j) {
+    const uint4* x = reinterpret_cast<const uint4*>(v + (int64_t)j * a.v_token);
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+      const uint4 y = __ldg(x + e);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        strange |= (w[b] & kMask) == kMask || ((w[b] >> 16) & kMask) == kMask;
+    }
+  }
+  if (!strange) return;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q + (int64_t)at * a.q_token +
+                                                  (int64_t)head * a.q_head);
+  const uint16_t* k = a.k + (int64_t)key0 * a.k_token + (int64_t)h * a.k_head;
+  float y[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+#pragma unroll 1
+  for (int j = 0; j < keys; ++j) {
+    const uint4* kj = reinterpret_cast<const uint4*>(k + (int64_t)j * a.k_token);
+    const uint4* vj = reinterpret_cast<const uint4*>(v + (int64_t)j * a.v_token);
+    float s = 0.0f;
+#pragma unroll 1
+    for (int d = 0; d < D / 8; ++d) {
+      const uint4 x = __ldg(q + d), z = __ldg(kj + d);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float2 u = unpack2<F16>(xs[b]), w = unpack2<F16>(zs[b]);
+        s = fmaf(u.x, w.x, fmaf(u.y, w.y, s));
+      }
+    }
+    const float p = unpack2<F16>(pack2<F16>(ex2(fmaf(s, a.c, -mc)), 0.0f)).x;
+    bool nan = true;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint4 z = __ldg(vj + d);
+      const uint32_t zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float2 w = unpack2<F16>(zs[b]);
+        const int e = 8 * d + 2 * b;
+        y[e] = fmaf(p, w.x, y[e]);
+        y[e + 1] = fmaf(p, w.y, y[e + 1]);
+        nan = nan && y[e] != y[e] && y[e + 1] != y[e + 1];
+      }
+    }
+    if (nan) break;  // and so they stay
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(y[e]);
 }
 
 template <int D, int F16, bool PAGED, int NT>
@@ -665,6 +732,19 @@ __global__ void __launch_bounds__(384, 1)  // 168 registers, with one row tile (
         if (mine && a.lse)
           a.lse[at * a.Hq + head] = l == 0.0f ? -INFINITY : (m * a.c + log2f(l)) * kLn2;
         uint16_t* dst = a.out + (int64_t)at * a.o_token + (int64_t)head * a.o_head;
+        float zero = 0.0f;  // or NaN, where o holds an infinity or a NaN
+        auto store = [&](int i, const uint32_t* o) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            y[e] = some && inv != 0.0f ? pack2<F16>(__uint_as_float(o[2 * e]) * inv,
+                                                    __uint_as_float(o[2 * e + 1]) * inv)
+                                       : 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(dst + i + 8 * e) =
+                make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        };
 #pragma unroll
         for (int i = 0; i < D; i += 32) {
           uint32_t o[32];
@@ -672,18 +752,24 @@ __global__ void __launch_bounds__(384, 1)  // 168 registers, with one row tile (
             tm_ld(to + i, o);
             ld_wait();
             ld_touch(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) zero = fmaf(__uint_as_float(o[e]), 0.0f, zero);
           }
-          if (mine) {
-            uint32_t y[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              y[e] = some && inv != 0.0f ? pack2<F16>(__uint_as_float(o[2 * e]) * inv,
-                                                      __uint_as_float(o[2 * e + 1]) * inv)
-                                         : 0u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(dst + i + 8 * e) =
-                  make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          if (mine) store(i, o);
+        }
+        const bool strange = mine && zero != 0.0f && l > 0.0f;
+        if (__any_sync(~0u, strange)) {
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tm_ld(to + i, o);
+            ld_wait();
+            ld_touch(o);
+            if (strange) {
+              kept_apart<D, F16>(a, w.h, head, (int)at, w.key0, keys, min(w.hi, tiles * kTile), i,
+                                 m == -INFINITY ? 0.0f : m * a.c, o);
+              store(i, o);
+            }
           }
         }
       }
@@ -1253,7 +1339,8 @@ int m3::attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int
                     const int32_t* cu_q, const int32_t* cu_k, float scale, void* out,
                     int64_t o_token, int64_t o_head, float* lse, int* err, void* cuda_stream) {
   if (dtype != M3_KV_BF16 && dtype != M3_KV_F16) return set_error(M3_EINVAL, "dtype");
-  if (n_seq < 0 || n_q < 0 || n_k < 0) return set_error(M3_EINVAL, "negative count");
+  if (n_seq < 0 || n_seq > 8192) return set_error(M3_EINVAL, "n_seq out of 0..8192");
+  if (n_q < 0 || n_k < 0) return set_error(M3_EINVAL, "negative count");
   if (D != 64 && D != 128) return set_error(M3_EINVAL, "D: 64 or 128");
   if (Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 64)
     return set_error(M3_EINVAL, "Hq: a multiple of Hkv, up to 64 times it");
@@ -1277,6 +1364,15 @@ int m3::attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int
   a.o_token = o_token;
   a.o_head = o_head;
   a.lse = lse;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
   a.err = err;
   a.Hq = Hq;
   a.Hkv = Hkv;

@@ -53,7 +53,8 @@ enum { M3_LOGITS_F32 = 0, M3_LOGITS_BF16 = 1, M3_LOGITS_F16 = 2 };
  *    cu[r] + i the position start + cached[r] + i, the request r, and the slot
  *    (-1 where it has no page).  Tokens past cu[n_req], the padding of a
  *    captured graph, get -1 in all three; tokens past n_tokens are dropped.
- * Sums past 2^31 - 1 stop there.  taken and free_at must be different words. */
+ * Sums past 2^31 - 1 stop there.  cu, lens and taken are other memory than fresh,
+ * cached and free_at. */
 M3_API int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
                      const int32_t* free_pages, int n_free, const int32_t* free_at, int32_t* table,
                      int max_pages, int64_t ld_table, int page, int n_pages, int start,
@@ -69,7 +70,7 @@ M3_API int m3_kv_store(int dtype, int n_tokens, int Hkv, int D, const void* k, i
                        int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
                        const int64_t* slots, void* pool, int n_pages, int page, void* cuda_stream);
 
-/* Causal attention of n_seq packed sequences: queries q [n_q][Hq][D], of
+/* Causal attention of n_seq (up to 8192) packed sequences: queries q [n_q][Hq][D], of
  * sequence s the rows cu_q[s]..cu_q[s + 1] - 1, keys and values k, v
  * [n_k][Hkv][D], rows cu_k[s]..cu_k[s + 1] - 1 (cu_k null: cu_q; then n_k = n_q).
  * The last query sits on the last key: of Lq queries and Lk keys query i
@@ -80,9 +81,9 @@ M3_API int m3_kv_store(int dtype, int n_tokens, int Hkv, int D, const void* k, i
  * cu_q[n_seq] are not computed and their outputs stay as they are.  Lengths
  * that the arrays do not hold are cut to what they do.
  * Scores, sums and lse are fp32; the weights are rounded to dtype before
- * their product with v.  Values of keys that a query does not attend to
- * never reach it unless they are infinite or NaN and belong to the same
- * sequence within the query's last 128 keys.
+ * their product with v.  Keys and values that a query does not attend to never
+ * reach it, infinities and NaN among them (those in values of a query's own
+ * sequence, up to 127 keys behind it, make its row slow).
  * D: 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 64; q, k, v, out 16-byte aligned with
  * strides that are multiples of 8; scale > 0. */
 M3_API int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int D,

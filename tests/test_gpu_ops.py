@@ -254,6 +254,36 @@ def test_prompt_other_sequences_and_bad_lengths(ops):
     assert torch.equal(out2[:70], out[:70]) and torch.equal(out2[130:], out[130:])
 
 
+@pytest.mark.parametrize("hq,hk,d,dtype", [(4, 1, 128, BF16), (2, 2, 64, F16)])
+def test_prompt_values_ahead_of_a_query_stay_there(ops, hq, hk, d, dtype):
+    # infinities and NaN in keys and values that later queries alone attend to
+    q, k, v, cu_q, cu_k = prompt_case([300, 150], [40, 0], hq, hk, d, dtype, 21, extra=0)
+    ends = [(0, 340), (340, 490)]
+    places = [(200, "v", math.nan), (205, "v", math.inf), (206, "v", -math.inf), (339, "v", math.nan), (339, "k", math.inf),
+              (350, "v", math.inf), (480, "v", math.nan), (485, "k", math.nan)]
+    for at, which, x in places:
+        (k if which == "k" else v)[at, 0, ::3 if at % 2 else 5] = x
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ops.m3_attn_prompt(q, k, v, i32(cu_q), out, lse, cu_k=i32(cu_k))
+    g = hq // hk
+    for (ka, kb), a, b in zip(ends, cu_q, cu_q[1:]):
+        n = kb - ka
+        for i in range(b - a):
+            seen = i + n - (b - a) + 1  # keys this query attends to
+            for h in range(hq):
+                z = (k[ka:ka + seen, h // g].double() @ q[a + i, h].double()) * d ** -0.5
+                p = torch.softmax(z, 0)[:, None] * v[ka:ka + seen, h // g].double()
+                want, got = p.sum(0), out[a + i, h].double()
+                if not bool(z.isfinite().all()):
+                    continue  # a score of its own is none
+                fin = want.isfinite()
+                assert torch.equal(got.isnan(), want.isnan()), (a + i, h)
+                assert torch.equal(got[want.isinf()], want[want.isinf()]), (a + i, h)
+                # as attention_bounds, with the mean of |v| and of the scores' terms bounded by their largest
+                tol = (3 * R.HALF[dtype] + 2.0 ** -10) * float(v[ka:ka + seen][v[ka:ka + seen].isfinite()].abs().max())
+                assert float((got - want)[fin].abs().max()) <= tol, (a + i, h)
+
+
 def test_prompt_many_sequences(ops):
     rnd = random.Random(4)
     fresh = [rnd.choice([0, 1, 2, 3, 17, 40]) for _ in range(300)]
@@ -346,6 +376,16 @@ def test_prefix_bad_pages_are_left_out(ops):
     out, lse = torch.empty_like(q), torch.empty(3, 8, device="cuda")
     ops.m3_attn_prefix(q, pool, i32(pages), 400, i32(table), i32([40, 70, 16]), out, lse)
     check_prefix(out, lse, q, shared, own, [40, 70, 16], 128 ** -0.5, BF16)
+
+
+def test_prefix_without_own_pages(ops):
+    # a table without columns: the prefix alone, and with none of it nothing
+    for prefix in (400, 0):
+        q, pool, pages, shared, table, own = prefix_case(2, prefix, [0, 0], 8, 2, 64, 16, BF16, 4)
+        none = torch.empty(2, 0, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(q, 7.0), torch.full((2, 8), 7.0, device="cuda")
+        ops.m3_attn_prefix(q, pool, i32(pages), prefix, none, i32([0, -1]), out, lse)
+        check_prefix(out, lse, q, shared, own, [0, -1], 64 ** -0.5, BF16)
 
 
 def test_prefix_strides_and_lengths_past_the_table(ops):

@@ -38,15 +38,15 @@ def test_binding_covers_the_operators():
 
 
 MAP = dict(n_req=2, fresh=P, cached=None, free=P, n_free=4, free_at=None, table=P, max_pages=3, ld=3,
-           page=16, n_pages=8, start=0, n_tokens=4, cu=P, positions=P, slots=P, seqs=P, lens=P, taken=P,
-           stream=None)
+           page=16, n_pages=8, start=0, n_tokens=4, cu=P + 64, positions=P, slots=P, seqs=P, lens=P + 128,
+           taken=P, stream=None)
 
 
 @pytest.mark.parametrize("bad", [dict(n_req=0), dict(n_req=8193), dict(page=24), dict(page=8), dict(page=2048),
                                  dict(n_free=-1), dict(max_pages=-1), dict(n_pages=-1), dict(start=-1),
                                  dict(n_tokens=-1), dict(ld=2), dict(fresh=None), dict(table=None), dict(cu=None),
                                  dict(slots=None), dict(taken=None), dict(free=None), dict(lens=None),
-                                 dict(free_at=P), dict(positions=P + 4), dict(slots=P + 8), dict(seqs=P + 4)])
+                                 dict(free_at=P), dict(lens=P + 4), dict(cu=P), dict(cached=P + 128), dict(cached=P + 72), dict(positions=P + 4), dict(slots=P + 8), dict(seqs=P + 4)])
 def test_map_refuses(bad):
     m3, _, lib = _lib()
     assert lib.m3_kv_map(*{**MAP, **bad}.values()) == m3.M3_EINVAL
@@ -69,7 +69,7 @@ PROMPT = dict(dtype=0, n_seq=1, n_q=4, n_k=4, hq=4, hk=2, d=64, q=P, qt=256, qh=
               vt=128, vh=64, cu_q=P, cu_k=None, scale=0.125, out=P, ot=256, oh=64, lse=None, stream=None)
 
 
-@pytest.mark.parametrize("bad", [dict(dtype=-1), dict(n_seq=-1), dict(n_q=-1), dict(n_k=3), dict(hq=3), dict(hk=0),
+@pytest.mark.parametrize("bad", [dict(dtype=-1), dict(n_seq=-1), dict(n_seq=8193), dict(n_q=-1), dict(n_k=3), dict(hq=3), dict(hk=0),
                                  dict(hq=130, hk=2), dict(d=96), dict(q=None), dict(k=None), dict(v=None), dict(out=None),
                                  dict(cu_q=None), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                                  dict(scale=float("inf")), dict(q=P + 8), dict(k=P + 2), dict(v=P + 8), dict(out=P + 8),
