@@ -4,7 +4,8 @@
 //                    of 128-key tiles; packed prompts (causal) or a shared
 //                    prefix in pages (partial results)
 //   attn_own_kernel  warp MMA: one row's query heads against its own pages
-//   attn_join_kernel joins the partial results of a row by log-sum-exp
+//   attn_join_kernel joins the partial results of a row by log-sum-exp (few
+//                    positions: the own kernel's CTAs do, as a cluster)
 #include <cudaTypedefs.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -61,6 +62,14 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, one MUFU instruction; 2
 // The running maximum is raised, and O rescaled, only when a row's maximum
 // has grown by more than 2^8 since (P then stays below 2^8, and sums and
 // products are relative to the same reference, so nothing is lost).
+//
+// What bounds it: a key tile of both row tiles is 2048 cycles of products and as
+// many of exponentials, and takes about 3300: a row tile's softmax (1850) and
+// then the rest of its O += P V, the next S and the hand-overs (1430), the other
+// row tile's in between.  2 x 9000 tokens, 32 heads on 8, D 128, bf16: 1.10 ms,
+// 1200 TFLOP/s (tensor pipe and MUFU each 56 % active under the profiler).  Short
+// prompts are bound by a CTA's own length, about 9 us for three key tiles, of
+// which 5 are its beginning and end (code that runs once is fetched then).
 constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
 constexpr float kRaise = 8.0f;       // log2 units
 
@@ -802,14 +811,18 @@ __global__ void __launch_bounds__(384, 1)  // 168 registers, with one row tile (
 // V by 16-byte asynchronous copies into its own ring, swizzled for ldmatrix;
 // S = Q K^T and O += P V on m16n8k16, fp32 softmax.  Positions past the length
 // and pages that are not there are filled with zeros, not read, and masked.
+// Bound by HBM: 16 rows of 700 to 4500 positions, 8 KV heads of 128, alone 136 MB
+// in 27 us, 5.0 TB/s, with the ramp at both ends; more, smaller CTAs measured
+// slower (8 per SM 40.7 against 37.4 us for the whole call).
 constexpr int kOwnWarps = 4;
 constexpr int kOwnTile = 16;
 constexpr int kOwnStages = 3;
+constexpr int kClusterMost = 8;  // splits that a cluster joins
 
 template <int D>
 constexpr size_t own_smem() {
   const size_t ring = (size_t)kOwnWarps * kOwnStages * 2 * kOwnTile * D * 2;
-  const size_t merge = (size_t)kOwnWarps * 16 * (D + 2) * 4;
+  const size_t merge = (size_t)(kOwnWarps + 1) * 16 * (D + 2) * 4;
   return ring > merge ? ring : merge;
 }
 
@@ -827,6 +840,10 @@ struct OwnArgs {
   float c;
   float* part_o;    // [splits][n_rows * Hq][D]
   float2* part_ml;  // [splits][n_rows * Hq]
+  // the splits of a row in one cluster: its result
+  uint16_t* out;
+  int64_t o_row, o_head;
+  float* lse;
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
@@ -835,7 +852,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) 
                : "memory");
 }
 
-template <int D, int F16>
+// CLUSTER: the splits of a row and KV head are a cluster, which joins them
+// through its shared memory and writes the row itself.
+template <int D, int F16, bool CLUSTER>
 __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs a) {
   constexpr int ROWB = D * 2, KS = D / 16, NTO = D / 8, CH = D / 8;
   extern __shared__ __align__(128) uint8_t own_raw[];
@@ -859,7 +878,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   const size_t rows = (size_t)a.n_rows * a.Hq;
   const int heads = min(16, a.grp - mt * 16);
   const size_t id0 = (size_t)split * rows + (size_t)b * a.Hq + g * a.grp + mt * 16;
-  if (t0 >= t1) {
+  if (!CLUSTER && t0 >= t1) {
     if (tid < heads) a.part_ml[id0 + tid] = make_float2(-INFINITY, 0.0f);
     if (blockIdx.x == 0) pdl_wait();
     return;
@@ -1017,6 +1036,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   __syncthreads();
   float* mo = reinterpret_cast<float*>(own_raw);        // [warp][16][D]
   float* mml = mo + kOwnWarps * 16 * D;                 // [warp][16][2]
+  float* co = mml + kOwnWarps * 16 * 2;                 // CLUSTER: the CTA's own [16][D]
+  float* cml = co + 16 * D;                             // [16][2]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = gid + 8 * h;
@@ -1047,9 +1068,70 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
 #pragma unroll
       for (int k = 0; k < kOwnWarps; ++k)
         if (f[k] != 0.0f) y += mo[(k * 16 + r) * D + d] * f[k];
-      a.part_o[(id0 + r) * D + d] = y;
+      if constexpr (CLUSTER) co[r * D + d] = y;
+      else a.part_o[(id0 + r) * D + d] = y;
     }
-    if (lane == 0) a.part_ml[id0 + r] = make_float2(mm, ll);
+    if (lane == 0) {
+      if constexpr (CLUSTER) {
+        cml[2 * r] = mm;
+        cml[2 * r + 1] = ll;
+      } else {
+        a.part_ml[id0 + r] = make_float2(mm, ll);
+      }
+    }
+  }
+  if constexpr (CLUSTER) {
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    // head by head over the cluster's CTAs, a warp each
+    const bool padding = a.lens[b] < 0;
+    for (int r = split * kOwnWarps + warp; r < heads && !padding; r += a.splits * kOwnWarps) {
+      // lane k has the max and sum of CTA k; a CTA without a key has (-inf, 0), o = 0
+      float mk = -INFINITY, ll = 0.0f, v[kClusterMost][D / 32];
+      if (lane < a.splits) {
+        const float2 ml = *reinterpret_cast<const float2*>(cluster.map_shared_rank(cml, lane) + 2 * r);
+        mk = ml.x;
+        ll = ml.y;
+      }
+#pragma unroll
+      for (int k = 0; k < kClusterMost; ++k) {  // all on their way at once
+        const float* o = cluster.map_shared_rank(co, min(k, a.splits - 1)) + r * D + 2 * lane;
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(o + 32 * i);
+          v[k][i] = x.x;
+          v[k][i + 1] = x.y;
+        }
+      }
+      float mm = mk;
+#pragma unroll
+      for (int o = 4; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+      const float f = mk == -INFINITY && ll == 0.0f ? 0.0f : ex2(mk - mm);
+      if (f != 0.0f) ll *= f;
+#pragma unroll
+      for (int o = 4; o; o >>= 1) ll += __shfl_xor_sync(~0u, ll, o);
+      mm = __shfl_sync(~0u, mm, 0);
+      ll = __shfl_sync(~0u, ll, 0);
+      float y[D / 32] = {};
+#pragma unroll
+      for (int k = 0; k < kClusterMost; ++k) {
+        const float fk = __shfl_sync(~0u, f, k);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          if (fk != 0.0f) y[i] += v[k][i] * fk;
+      }
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+      const int head = g * a.grp + mt * 16 + r;
+      uint16_t* dst = a.out + (int64_t)b * a.o_row + (int64_t)head * a.o_head;
+#pragma unroll
+      for (int i = 0; i < D / 32; i += 2)
+        *reinterpret_cast<uint32_t*>(dst + 2 * lane + 32 * i) =
+            ll == 0.0f ? 0u : pack2<F16>(y[i] * inv, y[i + 1] * inv);
+      if (lane == 0 && a.lse)
+        a.lse[(size_t)b * a.Hq + head] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    }
+    cluster.sync();  // the others may still read this CTA's memory
+    return;
   }
   // The launch before this one is the prefix, beside which this one ran.  One
   // CTA waits for its end, so that the end of this launch is that of both.
@@ -1058,7 +1140,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
 
 // ------------------------------------------------------------------ join ---
 // A row and query head: the parts' (max, sum, unnormalised o), D / 4 lanes a
-// part, the parts side by side, then one sum over those.
+// part, the parts side by side, then one sum over those.  A few dependent reads
+// of L2: 5 to 7 us at the end of a call, its launch hidden by the one before.
 struct JoinArgs {
   const float* part_o;
   const float2* part_ml;
@@ -1234,12 +1317,30 @@ cudaError_t launch_tc(int nt, int D, int f16, const CUtensorMap& tq, const CUten
 
 template <int D, int F16>
 cudaError_t launch_own_t(const OwnArgs& a, const JoinArgs& j, bool after_prefix, cudaStream_t st) {
+  if (a.out) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(attn_own_kernel<D, F16, true>, own_smem<D>(), done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.n_rows * a.Hkv * a.mtiles * a.splits));
+    cfg.blockDim = dim3(kOwnWarps * 32);
+    cfg.dynamicSmemBytes = own_smem<D>();
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_own_kernel<D, F16, true>, a);
+  }
   if (a.splits > 0) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(attn_own_kernel<D, F16>, own_smem<D>(), done);
+    cudaError_t e = allow_smem(attn_own_kernel<D, F16, false>, own_smem<D>(), done);
     const unsigned grid = (unsigned)((long long)a.n_rows * a.Hkv * a.mtiles * a.splits);
     if (e == cudaSuccess)
-      e = launch_ex(attn_own_kernel<D, F16>, dim3(grid), dim3(kOwnWarps * 32), own_smem<D>(), st,
+      e = launch_ex(attn_own_kernel<D, F16, false>, dim3(grid), dim3(kOwnWarps * 32), own_smem<D>(), st,
                     after_prefix, a);
     if (e != cudaSuccess) return e;
   }
@@ -1259,6 +1360,7 @@ constexpr long long kAlonePositions = 2048;  // rows x prefix, see plan_prefix
 struct PrefixPlan {
   int grp = 0, tpt = 0, nt = 0, units = 0;  // rows per row tile, row tiles of a CTA, such groups
   bool alone = false;                       // the prefix is read by every row for itself
+  bool cluster = false;                     // and a row's splits join in a cluster
   int pre_splits = 0, pre_tiles = 0;     // splits of the prefix, key tiles of each
   int mtiles = 0, own_splits = 0;
   int64_t rows = 0, bytes = 0;
@@ -1307,6 +1409,14 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
     p->pre_splits = (int)((key_tiles + p->pre_tiles - 1) / p->pre_tiles);
   }
   if (own > 0) p->own_splits = small_splits(own, p->alone ? prefix + own : own);
+  // Few positions and rows: up to eight splits of 128 positions, which one cluster
+  // joins in the same launch (4 rows, prefix 300: 6.3 against 7.7 us)
+  const long long small = (prefix + 127) / 128 + (own + 127) / 128;
+  p->cluster = (p->alone || prefix == 0) && small > 0 && small <= kClusterMost && ctas * small <= 4ll * nsm;
+  if (p->cluster) {
+    p->pre_splits = (int)((prefix + 127) / 128);
+    p->own_splits = (int)((own + 127) / 128);
+  }
   const int64_t parts = p->pre_splits + p->own_splits;
   p->bytes = ((parts * p->rows * 8 + 15) & ~(int64_t)15) + parts * p->rows * D * 4;
   if (p->bytes == 0) p->bytes = 16;
@@ -1389,8 +1499,8 @@ int m3::attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int
   if (!ok) return set_error(M3_EINVAL, "no tensor map for these strides");
   // every sequence's last unit may be short: at most one more unit each
   auto most = [&](int nt) { return n_q / (nt * a.tpt) + (n_seq < n_q ? n_seq : n_q); };
-  // one row tile per CTA where pairs would leave half of the SMs without work
-  const int nt = (long long)most(2) * Hkv * 2 <= sm_count() ? 1 : 2;
+  // one row tile per CTA while there is an SM for each
+  const int nt = (long long)most(1) * Hkv <= sm_count() ? 1 : 2;
   const long long units = most(nt);
   if (units * Hkv > INT_MAX) return set_error(M3_EINVAL, "too many tokens");
   OPS_CK(launch_tc<false>(nt, D, f16, tq, tk, tv, a, (unsigned)(units * Hkv),
@@ -1508,6 +1618,12 @@ extern "C" int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, con
   o.part_o = po + (int64_t)(pre - o.pre_splits) * p.rows * D;
   o.part_ml = ml + (int64_t)(pre - o.pre_splits) * p.rows;
   JoinArgs j{po, ml, lens, static_cast<uint16_t*>(out), o_row, o_head, lse, n_rows, Hq, (int)parts};
+  if (p.cluster && o.splits > 0) {
+    o.out = static_cast<uint16_t*>(out);
+    o.o_row = o_row;
+    o.o_head = o_head;
+    o.lse = lse;
+  }
   if (D == 128)
     OPS_CK(f16 ? (launch_own_t<128, 1>(o, j, shared, st)) : (launch_own_t<128, 0>(o, j, shared, st)));
   else
