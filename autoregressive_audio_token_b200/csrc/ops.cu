@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
 
 // The same in two launches, for logits that fill the GPU several times over:
 // there the waits of a run's history, between its loads and its stores, leave
-// HBM idle (192 x 200000, fp32: 95 us in one launch, 79 in two; 64 x 200000: 34
+// HBM idle (192 x 200000, fp32: 95 us in one launch, 78 in two; 64 x 200000: 34
 // and 32; 64 x 50000: 13.5 and 17.5).  The first streams the logits under the mask alone, with nothing to wait for; the
 // second takes up a row's noted tokens, kept in a hash table in shared memory
 // that it builds while the first one ends.
@@ -614,16 +614,21 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
     if (again) twice = 1;
     __syncthreads();
   }
-  // the taken slots side by side (one counter for every token would take the
-  // tokens one by one)
-  for (int i = tid; i < S; i += kTouchThreads) {
-    const unsigned taken = __ballot_sync(~0u, key[i] >= 0);
-    int base = 0;
-    if ((tid & 31) == 0 && taken) base = smem_add(&n_list, __popc(taken));
-    base = __shfl_sync(~0u, base, 0);
-    if ((taken >> (tid & 31)) & 1)
-      list[base + __popc(taken & ((1u << (tid & 31)) - 1))] = (uint16_t)i;
+  // the taken slots side by side: one addition to the counter per warp (one per
+  // token or per 32 slots, and they queue for it)
+  int mine = 0;
+  for (int i = tid; i < S; i += kTouchThreads) mine += key[i] >= 0;
+  int place = mine;  // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, place, o);
+    if ((tid & 31) >= o) place += v;
   }
+  int base = 0;
+  if ((tid & 31) == 31) base = smem_add(&n_list, place);
+  place += __shfl_sync(~0u, base, 31) - mine;
+  for (int i = tid; i < S; i += kTouchThreads)
+    if (key[i] >= 0) list[place++] = (uint16_t)i;
   const float rep = a.rep ? __ldg(a.rep + row) : 1.0f, freq = a.freq ? __ldg(a.freq + row) : 0.0f;
   const float pres = a.pres ? __ldg(a.pres + row) : 0.0f, inv = 1.0f / rep;
   const uint32_t* mask = nullptr;
