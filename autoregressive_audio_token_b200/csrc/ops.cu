@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
 
 // The same in two launches, for logits that fill the GPU several times over:
 // there the waits of a run's history, between its loads and its stores, leave
-// HBM idle (192 x 200000, fp32: 95 us in one launch, 78 in two; 64 x 200000: 34
+// HBM idle (192 x 200000, fp32: 95 us in one launch, 75 in two; 64 x 200000: 34
 // and 32; 64 x 50000: 13.5 and 17.5).  The first streams the logits under the mask alone, with nothing to wait for; the
 // second takes up a row's noted tokens, kept in a hash table in shared memory
 // that it builds while the first one ends.
@@ -566,6 +566,16 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
   const int lo = part * a.range, hi = min(a.vocab, lo + a.range);
   const unsigned span = (unsigned)max(hi - lo, 0);
   const int shift = __clz(S - 1);
+  const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
+  const float* val = a.bias + (size_t)row * a.n_bias;
+  const int32_t* hist = a.history ? a.history + row * a.ld_history : nullptr;
+  // asked for ahead of the table: the first of the history and of the biases
+  int first[kAtOnce], n_hist = a.n_history;
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u)
+    first[u] = hist && tid + u * kTouchThreads < n_hist ? __ldg(hist + tid + u * kTouchThreads) : -1;
+  if (hist && a.hist_len) n_hist = min(n_hist, max(0, __ldg(a.hist_len + row)));
+  const int id0 = tid < a.n_bias ? __ldg(ids + tid) : -1;
   for (int i = tid; i < S; i += kTouchThreads) {
     key[i] = -1;
     cnt[i] = 0;
@@ -581,17 +591,14 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
       h = (h + 1) & (S - 1);
     }
   };
-  const int32_t* ids = a.bias_ids + (size_t)row * a.n_bias;
-  const float* val = a.bias + (size_t)row * a.n_bias;
-  if (a.history) {
-    const int32_t* hist = a.history + row * a.ld_history;
-    int n = a.n_history;
-    if (a.hist_len) n = min(n, max(0, __ldg(a.hist_len + row)));
-    for (int i0 = tid; i0 < n; i0 += kAtOnce * kTouchThreads) {  // several loads under way
+  if (hist) {
+    for (int i0 = tid; i0 < n_hist; i0 += kAtOnce * kTouchThreads) {  // several loads under way
       int id[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
-        id[u] = i0 + u * kTouchThreads < n ? __ldg(hist + i0 + u * kTouchThreads) : -1;
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = i0 + u * kTouchThreads;
+        id[u] = i >= n_hist ? -1 : i0 == tid ? first[u] : __ldg(hist + i);
+      }
 #pragma unroll 1
       for (int u = 0; u < kAtOnce; ++u) {
         const int v = u == 0 ? id[0] : u == 1 ? id[1] : u == 2 ? id[2] : id[3];
@@ -600,19 +607,22 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
     }
   }
   // the first entry of each token owns it, whatever the order of the atomics
+  int slot0 = 0;  // of the thread's first entry
   for (int e = tid; e < a.n_bias; e += kTouchThreads) {
-    const int id = __ldg(ids + e);
-    if ((unsigned)id - (unsigned)lo < span) atomicMax(&code[slot_of(id)], a.n_bias - e);
+    const int id = e == tid ? id0 : __ldg(ids + e);
+    if ((unsigned)id - (unsigned)lo >= span) continue;
+    const int h = slot_of(id);
+    if (e == tid) slot0 = h;
+    atomicMax(&code[h], a.n_bias - e);
   }
   __syncthreads();
   if (biases) {
-    bool again = false;
-    for (int e = tid; e < a.n_bias; e += kTouchThreads) {
+    bool again = (unsigned)id0 - (unsigned)lo < span && code[slot0] != a.n_bias - tid;
+    for (int e = tid + kTouchThreads; e < a.n_bias; e += kTouchThreads) {
       const int id = __ldg(ids + e);
       if ((unsigned)id - (unsigned)lo < span) again |= code[slot_of(id)] != a.n_bias - e;
     }
     if (again) twice = 1;
-    __syncthreads();
   }
   // the taken slots side by side: one addition to the counter per warp (one per
   // token or per 32 slots, and they queue for it)
