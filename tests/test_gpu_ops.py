@@ -651,3 +651,54 @@ def test_refusals_leave_no_error_behind(ops):
         with pytest.raises(M3Error):
             call()
     ops.m3_ops_sync_status()
+
+
+def large_calls(ops, seed):
+    """The forms of many CTAs: a shared prefix beside the rows' own pages, logits in two launches, long prompts."""
+    lens = [(7 * i + seed) % 300 for i in range(40)]
+    q, pool, pages, shared, table, own = prefix_case(40, 2000, lens, 8, 2, 64, 32, BF16, seed)
+    o1, l1 = torch.zeros_like(q), torch.zeros(40, 8, device="cuda")
+    ws = torch.empty(ops.m3_attn_prefix_workspace(40, 8, 2, 64, len(pages), 32, len(table[0])), dtype=torch.uint8,
+                     device="cuda")
+    pages, table, lens_t = i32(pages), i32(table), i32(lens)
+    x = torch.randn(120, 130001, generator=gen(seed), device="cuda")
+    y = torch.zeros_like(x)
+    history, hist_len, rep, freq, pres, ids, bias, mask, row = rule_inputs(120, 130001, 600, 40, 3, seed)
+    p, k, v, cu_q, _ = prompt_case([2000, 700, 1500], [0, 0, 0], 8, 2, 128, F16, seed, extra=0)
+    o2, l2, cu = torch.zeros_like(p), torch.zeros(p.shape[:2], device="cuda"), i32(cu_q)
+
+    def run():
+        ops.m3_attn_prefix(q, pool, pages, 2000, table, lens_t, o1, l1, workspace=ws)
+        ops.m3_logit_rules(x, y, history, hist_len, rep, freq, pres, ids, bias, mask, row)
+        ops.m3_attn_prompt(p, k, v, cu, o2, l2)
+
+    return run, [o1, l1, y, o2, l2]
+
+
+def test_large_calls_captured_and_side_by_side(ops):
+    sets = [large_calls(ops, s) for s in (1, 2)]
+    torch.cuda.synchronize()
+    want, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for run, outs in sets:
+        run()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+    for (run, outs), st in zip(sets, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            run()
+            run()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _, outs in sets:
+        for o in outs:
+            o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(sets, want):
+        for i, (o, x) in enumerate(zip(outs, w)):
+            assert torch.equal(o, x), i
