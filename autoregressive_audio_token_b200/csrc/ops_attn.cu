@@ -1106,8 +1106,9 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
       float mm = mk;
 #pragma unroll
       for (int o = 4; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-      const float f = mk == -INFINITY && ll == 0.0f ? 0.0f : ex2(mk - mm);
-      if (f != 0.0f) ll *= f;
+      // (a factor may be 0 beside a far larger maximum, and takes the sum with it)
+      const float f = ll == 0.0f ? 0.0f : ex2(mk - mm);
+      ll *= f;
 #pragma unroll
       for (int o = 4; o; o >>= 1) ll += __shfl_xor_sync(~0u, ll, o);
       mm = __shfl_sync(~0u, mm, 0);
