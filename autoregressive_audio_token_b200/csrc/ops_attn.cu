@@ -1054,20 +1054,21 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   }
   __syncthreads();
   for (int r = warp; r < heads; r += kOwnWarps) {
+    // (a warp without a key has the sum 0; scores that are NaN leave the maximum
+    // as it is and make the sum NaN, whatever its factor)
     float mm = -INFINITY, f[kOwnWarps], ll = 0.0f;
 #pragma unroll
     for (int k = 0; k < kOwnWarps; ++k) mm = fmaxf(mm, mml[(k * 16 + r) * 2]);
 #pragma unroll
     for (int k = 0; k < kOwnWarps; ++k) {
-      const float mk = mml[(k * 16 + r) * 2];
-      f[k] = mk == -INFINITY ? 0.0f : ex2(mk - mm);
-      ll += mml[(k * 16 + r) * 2 + 1] * f[k];
+      const float mk = mml[(k * 16 + r) * 2], lk = mml[(k * 16 + r) * 2 + 1];
+      f[k] = lk == 0.0f ? 0.0f : ex2(mk - mm);
+      ll += lk * f[k];
     }
     for (int d = lane; d < D; d += 32) {
-      float y = 0.0f;
+      float y = 0.0f;  // o of a warp without a key is 0
 #pragma unroll
-      for (int k = 0; k < kOwnWarps; ++k)
-        if (f[k] != 0.0f) y += mo[(k * 16 + r) * D + d] * f[k];
+      for (int k = 0; k < kOwnWarps; ++k) y += mo[(k * 16 + r) * D + d] * f[k];
       if constexpr (CLUSTER) co[r * D + d] = y;
       else a.part_o[(id0 + r) * D + d] = y;
     }
@@ -1108,6 +1109,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
       for (int o = 4; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
       // (a factor may be 0 beside a far larger maximum, and takes the sum with it)
       const float f = ll == 0.0f ? 0.0f : ex2(mk - mm);
+      const unsigned have = __ballot_sync(~0u, ll != 0.0f);  // with a key; not the lanes past the last
       ll *= f;
 #pragma unroll
       for (int o = 4; o; o >>= 1) ll += __shfl_xor_sync(~0u, ll, o);
@@ -1119,7 +1121,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
         const float fk = __shfl_sync(~0u, f, k);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          if (fk != 0.0f) y[i] += v[k][i] * fk;
+          if ((have >> k) & 1) y[i] += v[k][i] * fk;
       }
       const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
       const int head = g * a.grp + mt * 16 + r;
@@ -1188,10 +1190,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const JoinArgs 
   float l = 0.0f;
   for (int p = tid; p < a.parts; p += T) {
     const float2 ml = __ldcg(a.part_ml + p * rows + id);
-    // a part without a key has no o
-    const float x = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ex2(ml.x - m);
-    f[r][p] = x;
-    if (x != 0.0f) l += ml.y * x;
+    // A part without a key has the sum 0 and no o: marked by a factor below 0.
+    // Every other one counts, also with the factor 0: its sum or o may be NaN
+    // (scores that are NaN leave the maximum as it is).
+    const float x = ex2(ml.x - m);
+    f[r][p] = ml.y == 0.0f ? -1.0f : x;
+    if (ml.y != 0.0f) l += ml.y * x;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
@@ -1207,7 +1211,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const JoinArgs 
 #pragma unroll 8
   for (int p = side; p < a.parts; p += SIDE) {
     const float x = f[r][p];
-    if (x == 0.0f) continue;
+    if (x < 0.0f) continue;
     const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (p * rows + id) * D + d));
     y.x += v.x * x;
     y.y += v.y * x;

@@ -33,6 +33,74 @@ def run_prefix(ops, f, q, pool, pages, table, scale=None):
     return out, lse
 
 
+def put(pool, pages, page, first, last, side, head, value):
+    """Positions first..last - 1 of these pages: K (side 0) or V (1) of a head."""
+    for p in range(first, last):
+        pool[pages[p // page], side, head, p % page] = value
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("first,last", [(128, 256), (0, 128), (200, 201)])
+def test_prefix_scores_that_are_no_numbers(ops, form, first, last):
+    # keys of NaN that a row attends to, a whole run of positions among them, make its result NaN
+    f, (q, pool, pages, shared, table, own) = case_of(form)
+    g = f["hq"] // f["hk"]
+    plain, plain_lse = run_prefix(ops, f, q, pool, pages, table)
+    put(pool, pages, f["page"], first, last, 0, 1, math.nan)
+    out, lse = run_prefix(ops, f, q, pool, pages, table)
+    hit = torch.zeros(f["hq"], dtype=torch.bool, device="cuda")
+    hit[g:2 * g] = True
+    assert bool(out[:, hit].isnan().all()) and bool(lse[:, hit].isnan().all())
+    assert torch.equal(out[:, ~hit], plain[:, ~hit]) and torch.equal(lse[:, ~hit], plain_lse[:, ~hit])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_prefix_own_scores_that_are_no_numbers(ops, form):
+    # among one row's own positions: that row alone
+    f, (q, pool, pages, shared, table, own) = case_of(form)
+    row = max(range(f["n"]), key=lambda b: f["lens"][b])
+    g, plain = f["hq"] // f["hk"], run_prefix(ops, f, q, pool, pages, table)
+    for first, last in ((0, 64), (f["lens"][row] - 1, f["lens"][row])):
+        put(pool, table[row], f["page"], first, last, 0, 0, math.nan)
+        out, lse = run_prefix(ops, f, q, pool, pages, table)
+        assert bool(out[row, :g].isnan().all()) and bool(lse[row, :g].isnan().all())
+        keep = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+        keep[row, :g] = False
+        assert torch.equal(out[keep], plain[0][keep]) and torch.equal(lse[keep], plain[1][keep])
+        put(pool, table[row], f["page"], first, last, 0, 0, 0.0)
+        plain = run_prefix(ops, f, q, pool, pages, table)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_prefix_infinite_values(ops, form):
+    # every weight is above 0: an infinite value comes out, and opposite ones make NaN; lse does not see them
+    f, (q, pool, pages, shared, table, own) = case_of(form)
+    g, (plain, plain_lse) = f["hq"] // f["hk"], run_prefix(ops, f, q, pool, pages, table)
+    for p, d, x in ((130, 3, math.inf), (140, 5, -math.inf), (10, 7, math.inf), (290, 7, -math.inf), (150, 9, math.nan)):
+        pool[pages[p // f["page"]], 1, 0, p % f["page"], d] = x
+    out, lse = run_prefix(ops, f, q, pool, pages, table)
+    assert torch.equal(lse, plain_lse)
+    assert bool((out[:, :g, 3] == math.inf).all()) and bool((out[:, :g, 5] == -math.inf).all())
+    assert bool(out[:, :g, 7].isnan().all()) and bool(out[:, :g, 9].isnan().all())
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[:, :g, [3, 5, 7, 9]] = False
+    assert torch.equal(out[keep], plain[keep])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_prefix_infinite_values_of_weights_too_small(ops, form):
+    # weights under the smallest number beside a far larger one: 0 times an infinity is no number, in every form
+    f, (q, pool, pages, shared, table, own) = case_of(form)
+    g, d = f["hq"] // f["hk"], f["d"]
+    for p in (10, 200):
+        for at, x in ((p, 12.0), (p ^ 128, -12.0)):
+            put(pool, pages, f["page"], at, at + 1, 0, 0, (x * torch.sign(q[0, 0].float())).to(f["dtype"]))
+        pool[pages[(p ^ 128) // f["page"]], 1, 0, (p ^ 128) % f["page"], 2] = math.inf
+        out, lse = run_prefix(ops, f, q, pool, pages, table, scale=0.25)
+        assert bool(out[0, 0, 2].isnan()) and bool(out[0, 0, 3:].isfinite().all()) and bool(lse.isfinite().all())
+        pool[pages[(p ^ 128) // f["page"]], 1, 0, (p ^ 128) % f["page"], 2] = 0.0
+
+
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("at", [0, 130, 299])
 def test_prefix_scores_far_apart(ops, form, at):
