@@ -8,6 +8,7 @@
 // to 4 us here).
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -214,9 +215,14 @@ void attn_prefix(const Tensor& q, const Tensor& pool, const Tensor& prefix_pages
     want(ws.device() == dev && ws.is_contiguous(),
          "workspace: a contiguous tensor on the same GPU is wanted");
   } else {
+    // From the stream's own memory: a block of the current stream's may still be
+    // in use there, and nothing makes the given stream wait for that.
+    c10::cuda::OptionalCUDAStreamGuard on_stream;
+    if (!stream.is_none())
+      on_stream.reset_stream(
+          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(on.stream), on.now));
     ws = at::empty({attn_prefix_workspace(n, hq, hk, d, npp, page, mp)},
                    at::TensorOptions().dtype(at::kByte).device(dev));
-    if (!stream.is_none()) py::cast(ws).attr("record_stream")(stream);
   }
   check(m3_attn_prefix(dt, count(n), count(hq), count(hk), count(d), qh.p, qh.row, qh.head, p,
                        count(pool.size(0)), count(page), pp, count(npp), count(prefix_len), tab,

@@ -4,6 +4,8 @@ same names.
 Native (csrc/ops_binding.cpp, module _ops): it checks shapes, types, devices
 and layouts and makes the library's calls.  Tensors are torch tensors of one
 GPU; the work goes to `stream`, by default the current stream of that GPU.
+Where it is another stream than a tensor's own, the caller orders the two and
+keeps the tensor (record_stream), as for any torch call on that stream.
 Outputs are the caller's tensors.  What is refused raises M3Error.  There is
 no CPU fallback: importing this module fails if _ops is missing.
 """

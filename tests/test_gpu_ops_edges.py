@@ -130,3 +130,53 @@ def test_prefix_shorter_than_its_pages(ops):
         for short in (1, 127, 130):
             out, lse = run_prefix(ops, {**f, "prefix": short}, q, pool, pages, table)
             T.check_prefix(out, lse, q, shared[:, :short], own, f["lens"], f["d"] ** -0.5, f["dtype"])
+
+
+def test_prefix_workspace_of_a_given_stream(ops):
+    # without a workspace the call takes one of the stream it runs on, not memory that the current stream has freed
+    # and may still be using
+    f, (q, pool, pages, shared, table, own) = case_of("shared", 8)
+    want = run_prefix(ops, f, q, pool, pages, table)
+    size = ops.m3_attn_prefix_workspace(f["n"], f["hq"], f["hk"], f["d"], len(pages), f["page"], len(table[0]))
+    pages_t, table_t, lens_t = i32(pages), i32(table), i32(f["lens"])
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    st = torch.cuda.Stream()
+    marks = torch.full((size,), 5, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    at, copy = marks.data_ptr(), torch.empty_like(marks)
+    torch.cuda._sleep(2_000_000)  # the current stream is busy, its copy from `marks` yet to come
+    copy.copy_(marks)
+    del marks
+    ops.m3_attn_prefix(q, pool, pages_t, f["prefix"], table_t, lens_t, out, lse, stream=st)
+    again = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == at  # still the current stream's
+    torch.cuda.synchronize()
+    assert bool((copy == 5).all())
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("current", ["captured", "other"])
+def test_prefix_workspace_of_a_captured_stream(ops, current):
+    # a captured call keeps its workspace for its replays, also when another stream is the current one
+    f, (q, pool, pages, shared, table, own) = case_of("shared", 8)
+    want = run_prefix(ops, f, q, pool, pages, table)
+    pages_t, table_t, lens_t = i32(pages), i32(table), i32(f["lens"])
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    st, other, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        with torch.cuda.stream(other if current == "other" else st):
+            ops.m3_attn_prefix(q, pool, pages_t, f["prefix"], table_t, lens_t, out, lse, stream=st)
+    size = ops.m3_attn_prefix_workspace(f["n"], f["hq"], f["hk"], f["d"], len(pages), f["page"], len(table[0]))
+    taken = []
+    for s in (torch.cuda.current_stream(), st, other):  # whoever asks now gets other memory
+        with torch.cuda.stream(s):
+            taken += [torch.full((size,), 5, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        out.zero_()
+        lse.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert all(bool((x == 5).all()) for x in taken)
