@@ -455,7 +455,6 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
     }
     if (w & kBiased) {
       // the run's few biases stand in no order: the token's are added in theirs
-      float b = 0.0f;
       for (int last = -1;;) {
         int e = INT_MAX;
         float v = 0.0f;
@@ -467,10 +466,9 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
           }
         }
         if (e == INT_MAX) break;
-        b += v;
+        x += v;
         last = e;
       }
-      x += b;
     }
     out[at] = from_f<T>(x);
   }
@@ -672,11 +670,10 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
       }
       if (ok[u] && biases && code[h[u]] > 0) {
         const int e = a.n_bias - code[h[u]];
-        float b = __ldg(val + e);
-        if (twice)  // some token has several entries: added up in their order
+        x += __ldg(val + e);
+        if (twice)  // some token has several entries: added in their order
           for (int f = e + 1; f < a.n_bias; ++f)
-            if (__ldg(ids + f) == at) b += __ldg(val + f);
-        x += b;
+            if (__ldg(ids + f) == at) x += __ldg(val + f);
       }
       if (ok[u]) out[at] = from_f<T>(x);
     }

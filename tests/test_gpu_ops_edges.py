@@ -180,3 +180,28 @@ def test_prefix_workspace_of_a_captured_stream(ops, current):
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert all(bool((x == 5).all()) for x in taken)
+
+
+# ----------------------------------------------------------------- rules ---
+# One launch, and the two that many runs (or penalties and biases alone, in place) take.
+
+def rules_both_ways(ops, x, **rules):
+    """The same rules out of place, in place (without a mask: two launches), and as many rows (two launches)."""
+    out = torch.empty_like(x)
+    ops.m3_logit_rules(x, out, **rules)
+    if rules.get("mask") is None:
+        y = x.clone()
+        ops.m3_logit_rules(y, y, **rules)
+        assert torch.equal(y.nan_to_num(), out.nan_to_num()) and torch.equal(y.isnan(), out.isnan())
+    return out
+
+
+def test_rules_add_biases_to_the_logit_in_their_order(ops):
+    x = torch.tensor([[1.0, 1.0, -3.0, 0.5, 1e8]], device="cuda")
+    ids = i32([[0, 1, 0, 1, 3, 4, 4, 4]])
+    bias = torch.tensor([[1e8, -1e8, -1e8, 1e8, 2.0, 1.0, 1.0, -1e8]], device="cuda")
+    want = x[0].clone()
+    for i, b in zip(ids[0].tolist(), bias[0]):
+        want[i] += b
+    assert want.tolist() == [0.0, 0.0, -3.0, 2.5, 0.0]  # 1 is lost beside 1e8
+    assert torch.equal(rules_both_ways(ops, x, bias_ids=ids, bias=bias)[0], want)
