@@ -440,16 +440,13 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
   if (!noted) return;
   __syncthreads();  // the notes are complete, and what this CTA wrote is there
 
-  // x / repetition as a product with its reciprocal: one more rounding in
-  // fp32, no division
-  const float inv = 1.0f / rep;
   for (int k = tid; k < n_list; k += kRuleThreads) {
     const int w = note[list[k]], at = (int)(s0 + list[k]);
     if (!allowed(at)) continue;
     float x = to_f(in[at]);  // from L1; out's, where that is logits, is the same
     const int c = w & (kBiased - 1);
     if (c > 0) {
-      x = x > 0.0f ? x * inv : x * rep;
+      x = x > 0.0f ? x / rep : x * rep;
       x -= freq * (float)c;
       x -= pres;
     }
@@ -638,7 +635,7 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
   for (int i = tid; i < S; i += kTouchThreads)
     if (key[i] >= 0) list[place++] = (uint16_t)i;
   const float rep = a.rep ? __ldg(a.rep + row) : 1.0f, freq = a.freq ? __ldg(a.freq + row) : 0.0f;
-  const float pres = a.pres ? __ldg(a.pres + row) : 0.0f, inv = 1.0f / rep;
+  const float pres = a.pres ? __ldg(a.pres + row) : 0.0f;
   const uint32_t* mask = nullptr;
   if (a.mask) {
     const int m = a.mask_row ? __ldg(a.mask_row + row) : (a.n_masks == 1 ? 0 : row);
@@ -664,7 +661,7 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
       const int at = key[h[u]], c = cnt[h[u]];
       float x = y[u];
       if (c > 0) {
-        x = x > 0.0f ? x * inv : x * rep;
+        x = x > 0.0f ? x / rep : x * rep;
         x -= freq * (float)c;
         x -= pres;
       }

@@ -205,3 +205,13 @@ def test_rules_add_biases_to_the_logit_in_their_order(ops):
         want[i] += b
     assert want.tolist() == [0.0, 0.0, -3.0, 2.5, 0.0]  # 1 is lost beside 1e8
     assert torch.equal(rules_both_ways(ops, x, bias_ids=ids, bias=bias)[0], want)
+
+
+def test_rules_divide_by_any_repetition(ops):
+    # quotients where 1 / repetition is no normal number, or rounds
+    rep = [1e-39, 1e-45, 3e38, 3.4e38, 3.0, 1.1]
+    x = torch.tensor([[2.5e-5, -1.0, 0.0, 1e-30, 7.3]] * len(rep), device="cuda")
+    r = torch.tensor(rep, device="cuda")
+    want = torch.where(x > 0, x / r[:, None], x * r[:, None])
+    got = rules_both_ways(ops, x, history=i32([[0, 1, 2, 3, 4]] * len(rep)), repetition=r)
+    assert torch.equal(got, want)
