@@ -762,11 +762,21 @@ extern "C" int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
   if (!fresh || !cu || !lens || !taken || (n_free && !free_pages) || (max_pages && !table) ||
       (n_tokens && (!positions || !slots || !seqs)))
     return set_error(M3_EINVAL, "null argument");
-  if (free_at == taken) return set_error(M3_EINVAL, "free_at and taken are the same word");
-  // every CTA reads the lengths while one writes the sums
-  for (const int32_t* in : {fresh, cached})
-    if (in && ((lens < in + n_req && in < lens + n_req) || (cu < in + n_req && in < cu + n_req + 1)))
-      return set_error(M3_EINVAL, "cu or lens overlaps fresh or cached");
+  // every CTA reads the inputs while others write
+  struct Span {
+    const void* p;
+    size_t bytes;
+  };
+  const size_t n = n_req, nt = n_tokens;
+  const Span ins[] = {{fresh, 4 * n}, {cached, 4 * n}, {free_pages, 4 * (size_t)n_free}, {free_at, 4}};
+  const Span outs[] = {{cu, 4 * (n + 1)}, {lens, 4 * n},  {taken, 4},
+                       {positions, 4 * nt}, {seqs, 4 * nt}, {slots, 8 * nt}};
+  for (const Span& i : ins)
+    for (const Span& o : outs) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(i.p), b = reinterpret_cast<uintptr_t>(o.p);
+      if (a && a < b + o.bytes && b < a + i.bytes)
+        return set_error(M3_EINVAL, "an output overlaps fresh, cached, free_pages or free_at");
+    }
   if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots) |
        reinterpret_cast<uintptr_t>(seqs)) & 15)
     return set_error(M3_EINVAL, "positions, slots and seqs have to be 16-byte aligned");

@@ -53,8 +53,8 @@ enum { M3_LOGITS_F32 = 0, M3_LOGITS_BF16 = 1, M3_LOGITS_F16 = 2 };
  *    cu[r] + i the position start + cached[r] + i, the request r, and the slot
  *    (-1 where it has no page).  Tokens past cu[n_req], the padding of a
  *    captured graph, get -1 in all three; tokens past n_tokens are dropped.
- * Sums past 2^31 - 1 stop there.  cu, lens and taken are other memory than fresh,
- * cached and free_at. */
+ * Sums past 2^31 - 1 stop there.  positions, seqs and slots are 16-byte aligned.
+ * The outputs are other memory than fresh, cached, free_pages and free_at. */
 M3_API int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
                      const int32_t* free_pages, int n_free, const int32_t* free_at, int32_t* table,
                      int max_pages, int64_t ld_table, int page, int n_pages, int start,

@@ -1,0 +1,38 @@
+"""Overlapping arguments of the serving operators, refused before anything is launched (no GPU needed)."""
+import pytest
+
+from test_ops_checks import _lib
+
+# disjoint, aligned addresses that are never followed
+MAP = dict(n_req=4, fresh=0x10000, cached=0x20000, free=0x30000, n_free=4, free_at=0x40000, table=0x50000, max_pages=3,
+           ld=3, page=16, n_pages=8, start=0, n_tokens=8, cu=0x60000, positions=0x70000, slots=0x80000, seqs=0x90000,
+           lens=0xA0000, taken=0xB0000, stream=None)
+INPUTS = dict(fresh=16, cached=16, free=16, free_at=4)
+OUTPUTS = dict(cu=20, lens=16, taken=4, positions=32, seqs=32, slots=64)
+
+
+def refusal(**changed):
+    m3, _, lib = _lib()
+    assert lib.m3_kv_map(*{**MAP, **changed}.values()) == m3.M3_EINVAL
+    return m3.m3_last_error()
+
+
+@pytest.mark.parametrize("i", INPUTS)
+@pytest.mark.parametrize("o", OUTPUTS)
+def test_map_outputs_are_no_inputs(i, o):
+    at = MAP[i]
+    wide = o in ("positions", "seqs", "slots")  # aligned to 16 bytes: the input is moved instead
+    for where in {0, INPUTS[i] - 4}:  # the output starts on the input's first word, on its last
+        moved = {i: MAP[o] - where} if wide else {o: at + where}
+        assert "an output overlaps" in refusal(**moved), where
+    last = OUTPUTS[o] - 4  # the input starts on the output's last word
+    assert "an output overlaps" in refusal(**{i: MAP[o] + last})
+
+
+@pytest.mark.parametrize("i", INPUTS)
+@pytest.mark.parametrize("o", OUTPUTS)
+def test_map_neighbours_are_no_overlap(i, o):
+    # what touches without overlapping gets as far as the next check, here an unaligned map
+    bad = "positions" if o == "seqs" else "seqs"
+    for at in (MAP[o] - INPUTS[i], MAP[o] + OUTPUTS[o]):
+        assert "16-byte aligned" in refusal(**{i: at, bad: MAP[bad] + 4})
