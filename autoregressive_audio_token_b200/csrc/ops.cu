@@ -856,7 +856,11 @@ extern "C" int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logi
   const uintptr_t ni = ((uintptr_t)(n_rows - 1) * ld_logits + vocab) * es;
   const uintptr_t no = ((uintptr_t)(n_rows - 1) * ld_out + vocab) * es;
   const bool same = i0 == o0 && (n_rows == 1 || ld_logits == ld_out);
-  if (!same && i0 < o0 + no && o0 < i0 + ni)
+  // rows of one stride may lie side by side, in columns of one buffer
+  const uintptr_t ld = (uintptr_t)ld_logits * es, row = (uintptr_t)vocab * es;
+  const uintptr_t apart = ld ? (o0 > i0 ? (o0 - i0) % ld : (ld - (i0 - o0) % ld) % ld) : 0;
+  const bool beside = n_rows > 1 && ld_logits == ld_out && apart >= row && apart + row <= ld;
+  if (!same && !beside && i0 < o0 + no && o0 < i0 + ni)
     return set_error(M3_EINVAL, "out overlaps logits without being logits");
   RuleArgs a{};
   a.in = logits;

@@ -215,3 +215,18 @@ def test_rules_divide_by_any_repetition(ops):
     want = torch.where(x > 0, x / r[:, None], x * r[:, None])
     got = rules_both_ways(ops, x, history=i32([[0, 1, 2, 3, 4]] * len(rep)), repetition=r)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rules_between_columns_of_one_buffer(ops, dtype):
+    # logits and out side by side in the same rows do not overlap
+    for n, gap in ((1000, 0), (1000, 13), (37, 3)):
+        buf = torch.zeros(3, 2 * n + gap, dtype=dtype, device="cuda")
+        for a, b in ((0, n + gap), (n + gap, 0)):
+            x, out = buf[:, a:a + n], buf[:, b:b + n]
+            x.copy_(torch.randn(3, n, generator=gen(n), device="cuda"))
+            want = x.clone()
+            ops.m3_logit_rules(x, out, bias_ids=i32([[5]] * 3), bias=torch.ones(3, 1, device="cuda"))
+            assert torch.equal(x, want)
+            want[:, 5] = (want[:, 5].float() + 1).to(dtype)
+            assert torch.equal(out, want)

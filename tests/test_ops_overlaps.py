@@ -1,7 +1,7 @@
 """Overlapping arguments of the serving operators, refused before anything is launched (no GPU needed)."""
 import pytest
 
-from test_ops_checks import _lib
+from test_ops_checks import RULES, _lib
 
 # disjoint, aligned addresses that are never followed
 MAP = dict(n_req=4, fresh=0x10000, cached=0x20000, free=0x30000, n_free=4, free_at=0x40000, table=0x50000, max_pages=3,
@@ -36,3 +36,14 @@ def test_map_neighbours_are_no_overlap(i, o):
     bad = "positions" if o == "seqs" else "seqs"
     for at in (MAP[o] - INPUTS[i], MAP[o] + OUTPUTS[o]):
         assert "16-byte aligned" in refusal(**{i: at, bad: MAP[bad] + 4})
+
+
+@pytest.mark.parametrize("x,out,ld", [(0, 1, 200), (0, 99, 200), (0, 101, 200), (99, 0, 200), (101, 0, 200), (0, 100, 199),
+                                      (100, 0, 199), (0, 199, 200), (0, 201, 200), (301, 0, 200), (0, 50, 100)])
+def test_rules_columns_that_overlap(x, out, ld):
+    # rows of 100 in one buffer of fp32 whose columns share places, in the same rows or the next
+    m3, _, lib = _lib()
+    base = RULES["x"]
+    call = {**RULES, "n": 3, "x": base + 4 * x, "out": base + 4 * out, "ldx": ld, "ldo": ld, "nm": 3}
+    assert lib.m3_logit_rules(*call.values()) == m3.M3_EINVAL
+    assert "out overlaps" in m3.m3_last_error()
