@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs
 // A CTA takes a run of one row's vocabulary.  It asks for everything it will
 // need at once -- its logits, the mask's words, the history, the biases -- then
 // notes in one word of shared memory per token how often the row's history has
-// it and whether a bias names it (additions and a flag: the order of the
-// atomics does not matter).  Meanwhile the logits are written out under the
+// it and whether a bias, or several, name it (additions and flags: the order of
+// the atomics does not matter).  Meanwhile the logits are written out under the
 // mask alone: few tokens have a word other than 0, and those are taken up again
 // afterwards, from a list, where the mask has left them as they were.  (Rules
 // inside the streaming loop bind the kernel by its instructions.)  Every run of
@@ -258,8 +258,34 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreArgs
 // 1500 tokens of history: 4.4 us, bound by the chain of its reads.
 constexpr int kRuleThreads = 512;
 constexpr int kRuleRun = 8192;  // logits of the longest run
-constexpr int kBiased = 1 << 30;  // of the word: a bias names the token; below it the count
+constexpr int kBiased = 1 << 30;  // of the word: a bias names the token; below them the count
+constexpr int kSeveral = 1 << 29;  // several do
+constexpr uint16_t kNoToken = 0xFFFF;
 constexpr int kRuleMaxBias = 4096, kRuleMaxHistory = 1 << 24;  // counts are exact in fp32
+
+// x plus the biases of a token in their order, among the entries from..n - 1:
+// a warp's work, 128 entries at a time.  For tokens that several entries name;
+// one with a single entry has it at hand.
+template <typename Token, typename Bias>
+__device__ __forceinline__ float add_biases(float x, int token, int from, int n, int lane,
+                                            Token token_of, Bias bias_of) {
+  for (int b = from; b < n; b += 128) {
+    bool is[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int e = b + 32 * q + lane;
+      is[q] = e < n && token_of(e) == token;
+    }
+    if (!__any_sync(~0u, is[0] || is[1] || is[2] || is[3])) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float v = is[q] ? bias_of(b + 32 * q + lane) : 0.0f;
+      for (unsigned m = __ballot_sync(~0u, is[q]); m; m &= m - 1)
+        x += __shfl_sync(~0u, v, __ffs(m) - 1);
+    }
+  }
+  return x;
+}
 
 // atom.shared as it stands: the compiler's own form for a counter gathers the
 // warp's lanes first, some 20 instructions at each place it is used.
@@ -298,6 +324,83 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ bool allows(const uint32_t* mask, int at) {
+  return !mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1);
+}
+// A logit under the penalties, its token c times in the history.
+__device__ __forceinline__ float penalise(float x, int c, float rep, float freq, float pres) {
+  if (c > 0) {
+    x = x > 0.0f ? x / rep : x * rep;
+    x -= freq * (float)c;
+    x -= pres;
+  }
+  return x;
+}
+
+// What a CTA of logit_rules_kernel has noted, in shared memory.
+struct RuleNotes {
+  const int* note;       // [run]
+  const uint16_t* list;  // tokens noted, from s0
+  int n_list;
+  uint16_t* named;       // [n_bias] the biases' tokens
+  float* bias;           // [n_bias]
+  int n_bias;
+  int* warp_sum;         // [warps]
+};
+
+// The tokens that several biases name: those entries side by side, in their
+// order, then a warp per token looks through them.  Out of line, since few calls
+// have such tokens and the rest of the kernel wants the registers.  4096 biases
+// on 80 x 8192 logits: 21 us a call with a token each, 188 all of one token, 945
+// two to a token; on 2 x 16385: 10, 178 and 19.
+template <typename T>
+__device__ __noinline__ void finish_several(const RuleNotes r, const T* in, T* out, long long s0,
+                                            const uint32_t* mask, float rep, float freq, float pres) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kEach = kRuleMaxBias / kRuleThreads;  // entries of a thread, in a row
+  const int per = (r.n_bias + kRuleThreads - 1) / kRuleThreads;
+  uint16_t token[kEach];
+  float value[kEach];
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = tid * per + i;
+    token[i] = i < per && e < r.n_bias ? r.named[e] : kNoToken;
+    if (token[i] != kNoToken && !(r.note[token[i]] & kSeveral)) token[i] = kNoToken;
+    value[i] = token[i] != kNoToken ? r.bias[e] : 0.0f;
+    mine += token[i] != kNoToken;
+  }
+  int place = mine;  // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, place, o);
+    if (lane >= o) place += v;
+  }
+  if (lane == 31) r.warp_sum[warp] = place;
+  __syncthreads();  // (every thread has its entries in registers)
+  int n_several = 0;
+  place -= mine;
+  for (int w = 0; w < kRuleThreads / 32; ++w) {
+    if (w < warp) place += r.warp_sum[w];
+    n_several += r.warp_sum[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (token[i] != kNoToken) {
+      r.named[place] = token[i];
+      r.bias[place++] = value[i];
+    }
+  __syncthreads();
+  for (int k = warp; k < r.n_list; k += kRuleThreads / 32) {
+    const int w = r.note[r.list[k]], at = (int)(s0 + r.list[k]);
+    if (!(w & kSeveral) || !allows(mask, at)) continue;
+    const float x = add_biases(
+        penalise(to_f(in[at]), w & (kSeveral - 1), rep, freq, pres), r.list[k], 0, n_several, lane,
+        [&](int e) { return r.named[e]; }, [&](int e) { return r.bias[e]; });
+    if (lane == 0) out[at] = from_f<T>(x);
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const RuleArgs a) {
@@ -354,11 +457,13 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
     val0 = __ldg(val + tid);
   }
   int* note = rule_smem;                                    // [run]
-  int4* named = reinterpret_cast<int4*>(rule_smem + a.run);  // [n_bias] (token, entry, bias)
-  uint16_t* list = reinterpret_cast<uint16_t*>(named + a.n_bias);  // [run] tokens noted, from s0
-  __shared__ int n_named, n_list;
+  // the biases and their tokens, counted from s0 (kNoToken: outside the run)
+  float* bias = reinterpret_cast<float*>(rule_smem + a.run);       // [n_bias]
+  uint16_t* named = reinterpret_cast<uint16_t*>(bias + a.n_bias);  // [n_bias]
+  uint16_t* list = named + a.n_bias;  // [run] tokens noted, from s0
+  __shared__ int n_list, several, warp_sum[kRuleThreads / 32];
   if (noted) {
-    if (tid == 0) n_named = n_list = 0;
+    if (tid == 0) n_list = several = 0;
     for (int i = tid * 4; i < a.run; i += kRuleThreads * 4)
       *reinterpret_cast<int4*>(note + i) = make_int4(0, 0, 0, 0);
     __syncthreads();
@@ -395,12 +500,19 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
   }
   if (biases) {
     auto name = [&](int e, int id, float b) {
-      if (id < lo || id >= hi) return;
-      if (smem_or(&note[(int)(id - s0)], kBiased) == 0)
-        list[smem_add(&n_list, 1)] = (uint16_t)(id - s0);
-      named[smem_add(&n_named, 1)] = make_int4(id, e, __float_as_int(b), 0);
+      const bool ours = id >= lo && id < hi;
+      const int at = (int)(id - s0);
+      named[e] = ours ? (uint16_t)at : kNoToken;
+      bias[e] = b;
+      if (!ours) return;
+      const int was = smem_or(&note[at], kBiased);
+      if (was == 0) list[smem_add(&n_list, 1)] = (uint16_t)at;
+      if (was & kBiased) {
+        smem_or(&note[at], kSeveral);
+        several = 1;
+      }
     };
-    name(tid, id0, val0);
+    if (tid < a.n_bias) name(tid, id0, val0);
     for (int e = tid + kRuleThreads; e < a.n_bias; e += kRuleThreads)
       name(e, __ldg(ids + e), __ldg(val + e));
   }
@@ -429,7 +541,7 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
       }
     }
   }
-  auto allowed = [&](int at) { return !mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1); };
+  auto allowed = [&](int at) { return allows(mask, at); };
   // its first and last few, where a 16-byte piece reaches past it
   const int head = (int)min((long long)hi, s0 + (lo - s0 + VEC - 1) / VEC * VEC);
   const int tail = (int)max((long long)head, s0 + (hi - s0) / VEC * VEC);
@@ -440,35 +552,23 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
   if (!noted) return;
   __syncthreads();  // the notes are complete, and what this CTA wrote is there
 
-  for (int k = tid; k < n_list; k += kRuleThreads) {
+  // (a noted token's logit comes from L1; out's, where that is logits, is the same)
+  auto penalised = [&](int at, int w) {
+    return penalise(to_f(in[at]), w & (kSeveral - 1), rep, freq, pres);
+  };
+  for (int k = tid; k < n_list; k += kRuleThreads) {  // those without a bias
     const int w = note[list[k]], at = (int)(s0 + list[k]);
-    if (!allowed(at)) continue;
-    float x = to_f(in[at]);  // from L1; out's, where that is logits, is the same
-    const int c = w & (kBiased - 1);
-    if (c > 0) {
-      x = x > 0.0f ? x / rep : x * rep;
-      x -= freq * (float)c;
-      x -= pres;
-    }
-    if (w & kBiased) {
-      // the run's few biases stand in no order: the token's are added in theirs
-      for (int last = -1;;) {
-        int e = INT_MAX;
-        float v = 0.0f;
-        for (int i = 0; i < n_named; ++i) {
-          const int4 n = named[i];
-          if (n.x == at && n.y > last && n.y < e) {
-            e = n.y;
-            v = __int_as_float(n.z);
-          }
-        }
-        if (e == INT_MAX) break;
-        x += v;
-        last = e;
-      }
-    }
-    out[at] = from_f<T>(x);
+    if (!(w & kBiased) && allowed(at)) out[at] = from_f<T>(penalised(at, w));
   }
+  if (!biases) return;
+  for (int e = tid; e < a.n_bias; e += kRuleThreads) {  // with one
+    if (named[e] == kNoToken) continue;
+    const int w = note[named[e]], at = (int)(s0 + named[e]);
+    if (!(w & kSeveral) && allowed(at)) out[at] = from_f<T>(penalised(at, w) + bias[e]);
+  }
+  if (!several) return;
+  finish_several<T>(RuleNotes{note, list, n_list, named, bias, a.n_bias, warp_sum}, in, out, s0, mask, rep,
+                    freq, pres);
 }
 
 // The same in two launches, for logits that fill the GPU several times over:
@@ -548,15 +648,15 @@ constexpr int kTouchThreads = 1024;
 constexpr int kAtOnce = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleArgs a) {
+__global__ void __launch_bounds__(kTouchThreads, 1) logit_touch_kernel(const RuleArgs a) {
   extern __shared__ int touch_raw[];
   const int S = a.slots;
   int* key = touch_raw;       // [S] token, or -1
   int* cnt = key + S;         // [S] times in the history
-  int* code = cnt + S;        // [S] n_bias - its first bias entry, or 0 (with biases)
+  int* code = cnt + S;        // [S] n_bias - its first bias entry, or 0; kSeveral (with biases)
   const bool biases = a.n_bias > 0;
   uint16_t* list = reinterpret_cast<uint16_t*>(touch_raw + S * (biases ? 3 : 2));
-  __shared__ int n_list, twice;
+  __shared__ int n_list;
   const int tid = threadIdx.x, row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
   const int lo = part * a.range, hi = min(a.vocab, lo + a.range);
   const unsigned span = (unsigned)max(hi - lo, 0);
@@ -576,7 +676,7 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
     cnt[i] = 0;
     if (biases) code[i] = 0;
   }
-  if (tid == 0) n_list = twice = 0;
+  if (tid == 0) n_list = 0;
   __syncthreads();
   auto slot_of = [&](int id) -> int {
     int h = (int)(((unsigned)id * 2654435761u) >> shift);  // multiplicative hashing (Knuth)
@@ -601,7 +701,9 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
       }
     }
   }
-  // the first entry of each token owns it, whatever the order of the atomics
+  // The first entry of each token owns it, whatever the order of the atomics.
+  // (4096 biases in place on 64 x 50000 logits: 26 us a call with a token each,
+  // 223 all of one token, 530 two to a token.)
   int slot0 = 0;  // of the thread's first entry
   for (int e = tid; e < a.n_bias; e += kTouchThreads) {
     const int id = e == tid ? id0 : __ldg(ids + e);
@@ -611,13 +713,12 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
     atomicMax(&code[h], a.n_bias - e);
   }
   __syncthreads();
-  if (biases) {
-    bool again = (unsigned)id0 - (unsigned)lo < span && code[slot0] != a.n_bias - tid;
-    for (int e = tid + kTouchThreads; e < a.n_bias; e += kTouchThreads) {
-      const int id = __ldg(ids + e);
-      if ((unsigned)id - (unsigned)lo < span) again |= code[slot_of(id)] != a.n_bias - e;
-    }
-    if (again) twice = 1;
+  // and the others say that there are several
+  for (int e = tid; e < a.n_bias; e += kTouchThreads) {
+    const int id = e == tid ? id0 : __ldg(ids + e);
+    if ((unsigned)id - (unsigned)lo >= span) continue;
+    const int h = e == tid ? slot0 : slot_of(id);
+    if ((code[h] & ~kSeveral) != a.n_bias - e) atomicOr(&code[h], kSeveral);
   }
   // the taken slots side by side: one addition to the counter per warp (one per
   // token or per 32 slots, and they queue for it)
@@ -644,13 +745,14 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
   T* out = static_cast<T*>(a.out) + row * a.ld_out;
   __syncthreads();
   pdl_wait();  // the logits are there
-  for (int k0 = tid; k0 < n_list; k0 += kAtOnce * kTouchThreads) {
+  const int lane = tid & 31;
+  for (int k0 = tid - lane; k0 < n_list; k0 += kAtOnce * kTouchThreads) {
     int h[kAtOnce];
     float y[kAtOnce];
     bool ok[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      const int k = k0 + u * kTouchThreads;
+      const int k = k0 + lane + u * kTouchThreads;
       h[u] = list[min(k, n_list - 1)];
       const int at = key[h[u]];
       ok[u] = k < n_list && (!mask || ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1));
@@ -659,18 +761,18 @@ __global__ void __launch_bounds__(kTouchThreads) logit_touch_kernel(const RuleAr
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int at = key[h[u]], c = cnt[h[u]];
-      float x = y[u];
-      if (c > 0) {
-        x = x > 0.0f ? x / rep : x * rep;
-        x -= freq * (float)c;
-        x -= pres;
-      }
-      if (ok[u] && biases && code[h[u]] > 0) {
-        const int e = a.n_bias - code[h[u]];
-        x += __ldg(val + e);
-        if (twice)  // some token has several entries: added in their order
-          for (int f = e + 1; f < a.n_bias; ++f)
-            if (__ldg(ids + f) == at) x += __ldg(val + f);
+      float x = penalise(y[u], c, rep, freq, pres);
+      if (biases) {
+        const int w = ok[u] ? code[h[u]] : 0, e = a.n_bias - (w & ~kSeveral);
+        if (w > 0 && !(w & kSeveral)) x += __ldg(val + e);
+        for (unsigned m = __ballot_sync(~0u, w & kSeveral); m; m &= m - 1) {
+          const int from = __ffs(m) - 1;
+          const float y = add_biases(
+              __shfl_sync(~0u, x, from), __shfl_sync(~0u, at, from), __shfl_sync(~0u, e, from),
+              a.n_bias, lane, [&](int f) { return __ldg(ids + f); },
+              [&](int f) { return __ldg(val + f); });
+          if (lane == from) x = y;
+        }
       }
       if (ok[u]) out[at] = from_f<T>(x);
     }
@@ -706,11 +808,11 @@ template <typename T>
 cudaError_t launch_rules(const RuleArgs& a, int n_rows, cudaStream_t st) {
   if (a.parts) return launch_rules_two<T>(a, n_rows, a.in != a.out || a.mask, st);
   const size_t smem =
-      a.history || a.n_bias ? 6 * (size_t)a.run + 16 * (size_t)a.n_bias : 0;
+      a.history || a.n_bias ? 6 * ((size_t)a.run + a.n_bias) : 0;
   if (smem > 40 * 1024) {  // past the default limit with what the kernel holds itself
     const cudaError_t e =
         cudaFuncSetAttribute(logit_rules_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             6 * kRuleRun + 16 * kRuleMaxBias);
+                             6 * (kRuleRun + kRuleMaxBias));
     if (e != cudaSuccess) return e;
   }
   logit_rules_kernel<T><<<(unsigned)(n_rows * a.runs), kRuleThreads, smem, st>>>(a);

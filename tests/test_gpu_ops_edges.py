@@ -217,6 +217,53 @@ def test_rules_divide_by_any_repetition(ops):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("n,r", [(8192, 80), (8192, 2), (60000, 3)])
+@pytest.mark.parametrize("ids", ["distinct", "one", "pairs"])
+def test_rules_with_the_most_biases(ops, n, r, ids):
+    g = gen(n + r)
+    x = torch.randn(r, n, generator=g, device="cuda")
+    which = torch.rand(r, n, generator=g, device="cuda").topk(4096).indices.to(torch.int32)
+    if ids == "one":
+        which[:] = 77
+    elif ids == "pairs":
+        which[:, 2048:] = which[:, :2048].flip(1)
+    bias = torch.randn(r, 4096, generator=g, device="cuda")
+    history = torch.randint(0, n, (r, 100), generator=g, device="cuda").to(torch.int32)
+    pen = torch.full((r,), 0.3, device="cuda")
+    want = x.clone()
+    for i in range(r):
+        seen, c = history[i].long().unique(return_counts=True)
+        want[i, seen] -= pen[i] * c
+    if ids == "one":
+        for e in range(4096):
+            want[:, 77] += bias[:, e]
+    else:
+        half = 2048 if ids == "pairs" else 4096
+        for part in range(0, 4096, half):  # the earlier entry of a token first
+            want.scatter_add_(1, which[:, part:part + half].long(), bias[:, part:part + half])
+    got = rules_both_ways(ops, x, history=history, frequency=pen, bias_ids=which, bias=bias)
+    # the penalty's product and difference may be one rounding or two: 2^-24 of their magnitudes each, and then the
+    # biases' additions round differently from there, each by as much
+    steps = 4 + (4096 if ids == "one" else 2)
+    mag = (x.abs() + 0.3 * 100 + (bias.abs().sum(1, keepdim=True) if ids == "one" else 2 * bias.abs().amax()))
+    assert bool(((got - want).abs() <= steps * 2.0 ** -23 * mag).all())
+
+
+def test_rules_time_of_the_most_biases(ops):
+    # far from the square of their number (a quarter of a second here): one token's are added one after another
+    x, out = torch.zeros(2, 16385, device="cuda"), torch.empty(2, 16385, device="cuda")
+    ids, bias = torch.full((2, 4096), 9, dtype=torch.int32, device="cuda"), torch.ones(2, 4096, device="cuda")
+    for to in (out, x):  # one launch; in place, the other form
+        ops.m3_logit_rules(x, to, bias_ids=ids, bias=bias)
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        ops.m3_logit_rules(x, to, bias_ids=ids, bias=bias)
+        end.record()
+        end.synchronize()
+        assert start.elapsed_time(end) < 20.0
+    assert out[0, 9] == 4096 and x[0, 9] == 2 * 4096
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_rules_between_columns_of_one_buffer(ops, dtype):
     # logits and out side by side in the same rows do not overlap
