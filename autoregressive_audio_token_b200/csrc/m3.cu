@@ -187,7 +187,6 @@ struct m3_ctx {
   // per prompt its length, cache row and first token
   int32_t *pr_seqs = nullptr, *pr_pos = nullptr, *pr_ints = nullptr;
   int64_t* pr_slots = nullptr;
-  int pr_cap = 0;                  // prompts pr_ints holds
   // the prefill GEMM's operands: a row-major copy of each bf16 layer's
   // projections (qkv | o | gate/up interleaved | down), made at the first
   // GEMM prefill from the tiled weights; stale once the layer is reloaded
@@ -1590,12 +1589,10 @@ extern "C" int m3_prefill_rows(m3_ctx* c, int n_rows, const int32_t* rows,
     if (!c->pr_seqs) CKR(dalloc(c, &c->pr_seqs, sizeof(int32_t) * P));
     if (!c->pr_pos) CKR(dalloc(c, &c->pr_pos, sizeof(int32_t) * P));
     if (!c->pr_slots) CKR(dalloc(c, &c->pr_slots, sizeof(int64_t) * P));
-    if (c->pr_cap < n_rows) {  // lengths, rows, first tokens (n + 1), sums, one word
-      CKR(dalloc(c, &c->pr_ints, sizeof(int32_t) * (4 * (size_t)c->kv_rows + 2)));
-      c->pr_cap = c->kv_rows;
-    }
+    // lengths, rows, first tokens (n + 1), sums, one word: for any cache's rows
+    if (!c->pr_ints) CKR(dalloc(c, &c->pr_ints, sizeof(int32_t) * (4 * (size_t)g.max_rows + 2)));
     CK(cudaMemcpyAsync(c->pr_ints, n_tokens, sizeof(int32_t) * n_rows, cudaMemcpyHostToDevice, c->st));
-    CK(cudaMemcpyAsync(c->pr_ints + c->pr_cap, rows, sizeof(int32_t) * n_rows, cudaMemcpyHostToDevice,
+    CK(cudaMemcpyAsync(c->pr_ints + g.max_rows, rows, sizeof(int32_t) * n_rows, cudaMemcpyHostToDevice,
                        c->st));
     CK(cudaStreamSynchronize(c->st));  // the caller's arrays
   }
@@ -1612,13 +1609,13 @@ extern "C" int m3_prefill_rows(m3_ctx* c, int n_rows, const int32_t* rows,
     CKR(enter(c));
     CK(cudaMemcpyAsync(c->pf_x, xs, sizeof(bf16) * T * H, cudaMemcpyDeviceToDevice, c->st));
     // which prompt and position each token is
-    int32_t *lens = c->pr_ints + i, *cu = c->pr_ints + 2 * c->pr_cap, *sums = cu + c->pr_cap + 1;
+    int32_t *lens = c->pr_ints + i, *cu = c->pr_ints + 2 * g.max_rows, *sums = cu + g.max_rows + 1;
     CKR(m3_kv_map(n, lens, nullptr, nullptr, 0, nullptr, nullptr, 0, 0, 16, 0, 0, T, cu, c->pr_pos,
-                  c->pr_slots, c->pr_seqs, sums, sums + c->pr_cap, c->st));
+                  c->pr_slots, c->pr_seqs, sums, sums + g.max_rows, c->st));
     rope_tokens_kernel<<<(T * (d / 2) + 255) / 256, 256, 0, c->st>>>(c->inv_freq, d / 2, c->pr_pos,
                                                                       T, c->pf_rope);
     CK(cudaGetLastError());
-    const PackedPrompts packed{n, cu, c->pr_ints + c->pr_cap + i};
+    const PackedPrompts packed{n, cu, c->pr_ints + g.max_rows + i};
     for (int l = 0; l < g.n_layers; ++l) CKR(record_prefill_layer(c, c->L[l], T, 0, l, &packed));
     int end = 0;
     for (int k = 0; k < n; ++k) {
