@@ -116,6 +116,54 @@ def test_prefix_scores_far_apart(ops, form, at):
     T.check_prefix(out, lse, q, shared, own, f["lens"], 0.25, f["dtype"])
 
 
+@pytest.mark.parametrize("n,prefix,page,d,dtype", [(3, 2500, 16, 128, BF16), (40, 2000, 64, 64, F16),
+                                                   (10, 3000, 256, 128, F16), (33, 2999, 16, 64, BF16),
+                                                   (5, 4600, 1024, 64, BF16), (2, 2100, 128, 128, BF16),
+                                                   (1, 2500, 16, 128, BF16)])  # the last: one row, no shared form
+def test_prefix_bad_pages_of_a_long_prefix(ops, n, prefix, page, d, dtype):
+    # missing pages in the first, a middle and the last key tile, a run of tiles without any page, and in rows' own
+    lens = [(97 * i + 700) % 900 for i in range(n)]
+    q, pool, pages, shared, table, own = T.prefix_case(n, prefix, lens, 8, 2, d, page, dtype, n)
+    last, bad = len(pages) - 1, [-1, pool.shape[0], 2**31 - 1, -2**31]
+    middle = list(range(len(pages) // 2, len(pages) // 2 + max(1, 256 // page)))  # two tiles or more
+    gone = sorted({0, *middle, last})
+    keep = torch.ones(prefix, dtype=torch.bool, device="cuda")
+    for i, p in enumerate(gone):
+        pages[p] = bad[i % 4]
+        keep[p * page:(p + 1) * page] = False
+    shared = shared[:, keep]
+    for b in range(0, n, 2):
+        if lens[b] > 0:
+            p = (lens[b] - 1) // page // 2
+            table[b][p] = bad[b % 4]
+            own[b] = torch.cat([own[b][:, :p * page], own[b][:, (p + 1) * page:]], 1)
+    out, lse = torch.full_like(q, 7.0), torch.full((n, 8), 7.0, device="cuda")
+    ops.m3_attn_prefix(q, pool, i32(pages), prefix, i32(table), i32(lens), out, lse)
+    T.check_prefix(out, lse, q, shared, own, lens, d ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("hq,hk,n", [(16, 1, 64), (16, 1, 65), (16, 1, 71), (64, 1, 16), (64, 1, 17), (5, 1, 200),
+                                     (33, 1, 24), (32, 8, 256)])
+@pytest.mark.parametrize("d,dtype,page,prefix", [(128, BF16, 64, 1000), (64, F16, 16, 1153)])
+def test_prefix_rows_of_two_tiles(ops, hq, hk, n, d, dtype, page, prefix):
+    # rows enough for CTAs of two row tiles, the second one short or empty
+    lens = [(11 * i) % 45 - 1 for i in range(n)]
+    q, pool, pages, shared, table, own = T.prefix_case(n, prefix, lens, hq, hk, d, page, dtype, n + hq)
+    out, lse = torch.full_like(q, 7.0), torch.full((n, hq), 7.0, device="cuda")
+    ops.m3_attn_prefix(q, pool, i32(pages), prefix, i32(table), i32(lens), out, lse)
+    T.check_prefix(out, lse, q, shared, own, lens, d ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (17, 1), (24, 4), (5, 1), (64, 1), (7, 7), (66, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_head_groups_of_a_long_prefix(ops, hq, hk, d):
+    lens = [3, 0, 190]
+    q, pool, pages, shared, table, own = T.prefix_case(3, 2133, lens, hq, hk, d, 32, BF16, hq)
+    out, lse = torch.empty_like(q), torch.empty(3, hq, device="cuda")
+    ops.m3_attn_prefix(q, pool, i32(pages), 2133, i32(table), i32(lens), out, lse, scale=0.11)
+    T.check_prefix(out, lse, q, shared, own, lens, 0.11, BF16)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_prefix_forms(ops, form):
     f, (q, pool, pages, shared, table, own) = case_of(form, 5)
