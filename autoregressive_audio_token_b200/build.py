@@ -4,13 +4,15 @@ native Python binding of its serving operators).
 Each .cu translation unit is compiled by its own nvcc process (in parallel),
 then linked into autoregressive_audio_token_b200/libm3.so with the CUDA
 runtime linked statically.  The binding is one C++ file against torch's
-headers, compiled beside them and linked to libm3.so.
+headers, compiled beside them and linked to libm3.so; without those or a C++
+compiler the library is built alone.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -52,12 +54,31 @@ def _compile(src: str, extra: list[str], bdir: str = BUILD) -> str:
     return obj
 
 
+def _binding_lacks() -> str | None:
+    """What the binding needs and this machine does not have (libm3.so needs none of it)."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return "torch"
+    for header in (os.path.join(torch.submodule_search_locations[0], "include", "torch", "csrc", "utils", "pybind.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return header
+    cxx = os.environ.get("CXX", "g++")
+    return None if shutil.which(cxx) else cxx
+
+
 def _compile_binding(force: bool) -> str | None:
-    """ops_binding.cpp's object where it is newer than the module, else None."""
+    """ops_binding.cpp's object where it is newer than the module, else None; None too where it
+    cannot be built here (said on stderr), and then a module older than its sources is removed."""
     deps = [BINDING_SRC, os.path.abspath(__file__)] + \
         [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     if not force and os.path.exists(BINDING) and \
             os.path.getmtime(BINDING) >= max(os.path.getmtime(f) for f in deps):
+        return None
+    if lacks := _binding_lacks():
+        sys.stderr.write(f"_ops, the binding of the serving operators, is not built: {lacks} is missing\n")
+        if os.path.exists(BINDING) and os.path.getmtime(BINDING) < max(os.path.getmtime(f) for f in deps):
+            os.remove(BINDING)
         return None
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     os.makedirs(BUILD, exist_ok=True)

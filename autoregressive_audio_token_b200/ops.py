@@ -12,8 +12,12 @@ no CPU fallback: importing this module fails if _ops is missing.
 from __future__ import annotations
 
 from . import m3 as _m3  # noqa: F401  (loads libm3.so)
-from ._ops import (m3_attn_prefix, m3_attn_prefix_workspace, m3_attn_prompt,  # noqa: F401
-                   m3_kv_map, m3_kv_store, m3_logit_rules, m3_ops_sync_status)
+try:
+    from ._ops import (m3_attn_prefix, m3_attn_prefix_workspace, m3_attn_prompt,  # noqa: F401
+                       m3_kv_map, m3_kv_store, m3_logit_rules, m3_ops_sync_status)
+except ModuleNotFoundError as e:
+    raise ImportError("_ops is missing: build it with `python -m autoregressive_audio_token_b200.build`, which says "
+                      "what it needs besides libm3.so (no CPU fallback)") from e
 
 EXPORTED = ("m3_kv_map", "m3_kv_store", "m3_attn_prompt", "m3_attn_prefix_workspace",
             "m3_attn_prefix", "m3_logit_rules", "m3_ops_sync_status")
