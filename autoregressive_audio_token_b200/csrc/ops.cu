@@ -406,7 +406,7 @@ template <typename T>
 __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const RuleArgs a) {
   constexpr int VEC = 16 / sizeof(T);
   constexpr int KV = kRuleRun / (VEC * kRuleThreads);  // 16-byte pieces per thread
-  extern __shared__ int rule_smem[];
+  extern __shared__ __align__(16) int rule_smem[];  // cleared 16 bytes at a time
   const int tid = threadIdx.x;
   const int row = blockIdx.x / a.runs, part = blockIdx.x % a.runs;
   const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
