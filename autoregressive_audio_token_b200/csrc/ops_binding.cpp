@@ -255,6 +255,8 @@ void logit_rules(const Tensor& logits, const Tensor& out, const Maybe& history,
     ldh = history->stride(0);
   }
   want(bias_ids.has_value() == bias.has_value(), "bias_ids and bias come together");
+  want(!bias || bias->dim() == 2, "bias: a tensor [rows, n] is wanted");
+  want(!mask || mask->dim() == 2, "mask: a tensor [masks, words] is wanted");
   const int64_t nb = bias ? bias->size(-1) : 0;
   const int64_t nm = mask ? mask->size(0) : 0;
   const auto* hl = arr<int32_t>("hist_len", hist_len, at::kInt, {r}, dev);

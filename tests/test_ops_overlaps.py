@@ -1,5 +1,6 @@
-"""Overlapping arguments of the serving operators, refused before anything is launched (no GPU needed)."""
+"""Overlapping and misshapen arguments of the serving operators, refused before anything is launched (no GPU needed)."""
 import pytest
+import torch
 
 from test_ops_checks import RULES, _lib
 
@@ -47,3 +48,16 @@ def test_rules_columns_that_overlap(x, out, ld):
     call = {**RULES, "n": 3, "x": base + 4 * x, "out": base + 4 * out, "ldx": ld, "ldo": ld, "nm": 3}
     assert lib.m3_logit_rules(*call.values()) == m3.M3_EINVAL
     assert "out overlaps" in m3.m3_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(bias_ids=torch.zeros(2, 1, dtype=torch.int32), bias=torch.tensor(1.0)),
+                                 dict(bias_ids=torch.tensor(3, dtype=torch.int32), bias=torch.tensor(1.0)),
+                                 dict(bias_ids=torch.zeros(2, dtype=torch.int32), bias=torch.zeros(2)),
+                                 dict(mask=torch.tensor(0, dtype=torch.int32)), dict(mask=torch.zeros(1, dtype=torch.int32)),
+                                 dict(history=torch.tensor(1, dtype=torch.int32))])
+def test_rules_of_too_few_dimensions(bad):
+    m3, ops, _ = _lib()
+    x = torch.zeros(2, 8)
+    with pytest.raises(m3.M3Error) as e:
+        ops.m3_logit_rules(x, x, **bad)
+    assert e.value.code == m3.M3_EINVAL
