@@ -1054,21 +1054,23 @@ __global__ void __launch_bounds__(kOwnWarps * 32) attn_own_kernel(const OwnArgs 
   }
   __syncthreads();
   for (int r = warp; r < heads; r += kOwnWarps) {
-    // (a warp without a key has the sum 0; scores that are NaN leave the maximum
-    // as it is and make the sum NaN, whatever its factor)
+    // A warp without a key has the sum 0, marked by a factor below 0.  Scores
+    // that are NaN leave the maximum as it is and make the sum NaN, whatever its
+    // factor.
     float mm = -INFINITY, f[kOwnWarps], ll = 0.0f;
 #pragma unroll
     for (int k = 0; k < kOwnWarps; ++k) mm = fmaxf(mm, mml[(k * 16 + r) * 2]);
 #pragma unroll
     for (int k = 0; k < kOwnWarps; ++k) {
       const float mk = mml[(k * 16 + r) * 2], lk = mml[(k * 16 + r) * 2 + 1];
-      f[k] = lk == 0.0f ? 0.0f : ex2(mk - mm);
-      ll += lk * f[k];
+      f[k] = lk == 0.0f ? -1.0f : ex2(mk - mm);
+      if (lk != 0.0f) ll += lk * f[k];
     }
     for (int d = lane; d < D; d += 32) {
-      float y = 0.0f;  // o of a warp without a key is 0
+      float y = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kOwnWarps; ++k) y += mo[(k * 16 + r) * D + d] * f[k];
+      for (int k = 0; k < kOwnWarps; ++k)
+        if (f[k] >= 0.0f) y += mo[(k * 16 + r) * D + d] * f[k];
       if constexpr (CLUSTER) co[r * D + d] = y;
       else a.part_o[(id0 + r) * D + d] = y;
     }
