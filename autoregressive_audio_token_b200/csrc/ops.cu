@@ -573,10 +573,13 @@ __global__ void __launch_bounds__(kRuleThreads, 3) logit_rules_kernel(const Rule
 
 // The same in two launches, for logits that fill the GPU several times over:
 // there the waits of a run's history, between its loads and its stores, leave
-// HBM idle (192 x 200000, fp32: 95 us in one launch, 75 in two; 64 x 200000: 34
-// and 32; 64 x 50000: 13.5 and 17.5).  The first streams the logits under the mask alone, with nothing to wait for; the
-// second takes up a row's noted tokens, kept in a hash table in shared memory
-// that it builds while the first one ends.
+// HBM idle.  (Us a call in one launch and in two, 4096 tokens of history and 300
+// biases: 192 x 200000 93 and 86 in fp32, 74 and 58 in 16 bits; 80 x 200000 44 and
+// 37, 33 and 27; 64 x 200000, which stays in one, 35 and 31, 27 and 26; 192 x 50000
+// 33 and 36, 28 and 33; 64 x 50000 15 and 20, 13 and 19.)  The first streams the
+// logits under the mask alone, with nothing to wait for; the second takes up a
+// row's noted tokens, kept in a hash table in shared memory that it builds while
+// the first one ends.
 constexpr int kMaskThreads = 256;
 constexpr int kMaskPieces = 4;
 

@@ -66,9 +66,10 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, one MUFU instruction; 2
 // What bounds it: a key tile of both row tiles is 2048 cycles of products and as
 // many of exponentials, and takes about 3300: a row tile's softmax (1850) and
 // then the rest of its O += P V, the next S and the hand-overs (1430), the other
-// row tile's in between.  2 x 9000 tokens, 32 heads on 8, D 128, bf16: 1.10 ms,
-// 1200 TFLOP/s (tensor pipe and MUFU each 56 % active under the profiler).  Short
-// prompts are bound by a CTA's own length, about 9 us for three key tiles, of
+// row tile's in between.  2 x 9000 tokens, 32 heads on 8, D 128, bf16: 1.29 ms,
+// 1030 TFLOP/s, under the power cap that a run of seconds meets; 1.10 ms, 1200
+// TFLOP/s, in runs too short for it (tensor pipe and MUFU each 56 % active under
+// the profiler).  Short prompts are bound by a CTA's own length, about 9 us for three key tiles, of
 // which 5 are its beginning and end (code that runs once is fetched then).
 constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
 constexpr float kRaise = 8.0f;       // log2 units
@@ -1363,7 +1364,8 @@ cudaError_t launch_own_t(const OwnArgs& a, const JoinArgs& j, bool after_prefix,
 
 constexpr long long kAlonePositions = 2048;  // rows x prefix, see plan_prefix
 
-// How m3_attn_prefix splits its work; the workspace follows from it.
+// How m3_attn_prefix splits its work; the workspace follows from it.  It goes by
+// the prefix's pages and the table's width: the rows' lengths live on the device.
 struct PrefixPlan {
   int grp = 0, tpt = 0, nt = 0, units = 0;  // rows per row tile, row tiles of a CTA, such groups
   bool alone = false;                       // the prefix is read by every row for itself
@@ -1402,8 +1404,11 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   };
   // A short prefix, or one row: every row reads it for itself, in one launch with
-  // its own positions (4 rows x 300: 6.7 against 9.7 us; 16 x 300: 13.1 against
-  // 11.2; 2 x 4500: 15.2 against 13.4)
+  // its own positions.  (Calls of 1 to 16 rows with prefixes of 128 to 4500, 40 own
+  // positions, 32 heads on 8 of 128, in pages of 64, 256 and 1024: the two meet
+  // between 2048 and 4096 rows x positions.  4 x 300 in pages of 256: 8.3 against
+  // 12.4 us; 4 x 1024: 14.4 against 12.4; 16 x 300 in pages of 64: 16.0 against
+  // 14.4; one row of 4500 with a table of 36 pages: 14.4 against 18.5.)
   p->alone = key_tiles > 0 && (n_rows == 1 || n_rows * prefix <= kAlonePositions);
   if (p->alone) {
     p->pre_splits = small_splits(prefix, prefix + own);
@@ -1417,7 +1422,8 @@ bool plan_prefix(int n_rows, int Hq, int Hkv, int D, int prefix_pages, int page,
   }
   if (own > 0) p->own_splits = small_splits(own, p->alone ? prefix + own : own);
   // Few positions and rows: up to eight splits of 128 positions, which one cluster
-  // joins in the same launch (4 rows, prefix 300: 6.3 against 7.7 us)
+  // joins in the same launch (4 rows, prefix 300: 6.3 against 7.7 us; with a table of
+  // 36 pages of 256, which does not fit eight splits, 12.4 a call against 8.3)
   const long long small = (prefix + 127) / 128 + (own + 127) / 128;
   p->cluster = (p->alone || prefix == 0) && small > 0 && small <= kClusterMost && ctas * small <= 4ll * nsm;
   if (p->cluster) {

@@ -84,6 +84,8 @@ M3_API int m3_kv_store(int dtype, int n_tokens, int Hkv, int D, const void* k, i
  * their product with v.  Keys and values that a query does not attend to never
  * reach it, infinities and NaN among them (those in values of a query's own
  * sequence, up to 127 keys behind it, make its row slow).
+ * A row whose scores are all -inf counts as one without a key; out is other
+ * memory than q, k and v.
  * D: 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 64; q, k, v, out 16-byte aligned with
  * strides that are multiples of 8; scale > 0. */
 M3_API int m3_attn_prompt(int dtype, int n_seq, int n_q, int n_k, int Hq, int Hkv, int D,
@@ -108,10 +110,12 @@ M3_API int64_t m3_attn_prefix_workspace(int n_rows, int Hq, int Hkv, int D, int 
  * outside 0..n_pages - 1 are left out.  What lies in the pages past a length
  * does not matter.
  *  n_prefix_pages: entries of prefix_pages, ceil(prefix_len / page) at least.
+ *  The work is split by n_prefix_pages and max_pages, not by the lengths: a
+ *    table no wider than the rows need is faster where rows are few.
  *  workspace: of m3_attn_prefix_workspace's size for this n_prefix_pages,
  *    16-byte aligned, the call's own while it runs; calls (and captured
  *    graphs) that may run at once need one each.
- * Types and alignment as m3_attn_prompt. */
+ * Types, alignment and memory as m3_attn_prompt. */
 M3_API int m3_attn_prefix(int dtype, int n_rows, int Hq, int Hkv, int D, const void* q,
                           int64_t q_row, int64_t q_head, const void* pool, int n_pages, int page,
                           const int32_t* prefix_pages, int n_prefix_pages, int prefix_len,
@@ -145,7 +149,10 @@ M3_API int m3_logit_rules(int dtype, int n_rows, int vocab, const void* logits, 
 
 /* Synchronise `cuda_stream` and return the first error that a kernel of this
  * header recorded on the current device since the last call (M3_ETIMEOUT),
- * clearing it, or M3_OK. */
+ * clearing it, or M3_OK.  One word serves all callers of the device: whoever asks
+ * first gets the error, and what any of them computed since the last M3_OK is in
+ * doubt.  Until it is cleared, waits that last over a millisecond (no sound one
+ * does) give up early. */
 M3_API int m3_ops_sync_status(void* cuda_stream);
 
 #ifdef __cplusplus
