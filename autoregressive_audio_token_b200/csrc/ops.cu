@@ -879,7 +879,7 @@ extern "C" int m3_kv_map(int n_req, const int32_t* fresh, const int32_t* cached,
   for (const Span& i : ins)
     for (const Span& o : outs) {
       const uintptr_t a = reinterpret_cast<uintptr_t>(i.p), b = reinterpret_cast<uintptr_t>(o.p);
-      if (a && a < b + o.bytes && b < a + i.bytes)
+      if (a && i.bytes && a < b + o.bytes && b < a + i.bytes)
         return set_error(M3_EINVAL, "an output overlaps fresh, cached, free_pages or free_at");
     }
   if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots) |

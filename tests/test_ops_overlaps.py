@@ -39,6 +39,12 @@ def test_map_neighbours_are_no_overlap(i, o):
         assert "16-byte aligned" in refusal(**{i: at, bad: MAP[bad] + 4})
 
 
+@pytest.mark.parametrize("o", OUTPUTS)
+def test_map_a_list_without_pages_overlaps_nothing(o):
+    bad = "positions" if o == "seqs" else "seqs"
+    assert "16-byte aligned" in refusal(free=MAP[o] + 4 * (OUTPUTS[o] > 4), n_free=0, **{bad: MAP[bad] + 4})
+
+
 @pytest.mark.parametrize("x,out,ld", [(0, 1, 200), (0, 99, 200), (0, 101, 200), (99, 0, 200), (101, 0, 200), (0, 100, 199),
                                       (100, 0, 199), (0, 199, 200), (0, 201, 200), (301, 0, 200), (0, 50, 100)])
 def test_rules_columns_that_overlap(x, out, ld):
