@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kTouchThreads, 1) logit_touch_kernel(const Rul
   __syncthreads();
   auto slot_of = [&](int id) -> int {
     int h = (int)(((unsigned)id * 2654435761u) >> shift);  // multiplicative hashing (Knuth)
-    for (;;) {  // ends: the tokens are fewer than the slots
+    for (;;) {  // ends: each entry comes here once, and they are fewer than the slots
       const int was = atomicCAS(&key[h], -1, id);
       if (was == -1 || was == id) return h;
       h = (h + 1) & (S - 1);
@@ -720,8 +720,11 @@ __global__ void __launch_bounds__(kTouchThreads, 1) logit_touch_kernel(const Rul
   for (int e = tid; e < a.n_bias; e += kTouchThreads) {
     const int id = e == tid ? id0 : __ldg(ids + e);
     if ((unsigned)id - (unsigned)lo >= span) continue;
-    const int h = e == tid ? slot0 : slot_of(id);
-    if ((code[h] & ~kSeveral) != a.n_bias - e) atomicOr(&code[h], kSeveral);
+    int h = e == tid ? slot0 : (int)(((unsigned)id * 2654435761u) >> shift);
+    while (key[h] != id && key[h] >= 0) h = (h + 1) & (S - 1);
+    // (an id read again that is not there, since somebody has written it
+    // meanwhile, neither takes a slot nor counts)
+    if (key[h] == id && (code[h] & ~kSeveral) != a.n_bias - e) atomicOr(&code[h], kSeveral);
   }
   // the taken slots side by side: one addition to the counter per warp (one per
   // token or per 32 slots, and they queue for it)
