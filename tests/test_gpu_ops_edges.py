@@ -188,16 +188,18 @@ def test_prefix_workspace_of_a_given_stream(ops):
     size = ops.m3_attn_prefix_workspace(f["n"], f["hq"], f["hk"], f["d"], len(pages), f["page"], len(table[0]))
     pages_t, table_t, lens_t = i32(pages), i32(table), i32(f["lens"])
     out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
-    st = torch.cuda.Stream()
-    marks = torch.full((size,), 5, dtype=torch.uint8, device="cuda")
+    held = lambda s: [x for x in torch.cuda.memory_snapshot() if x["stream"] == s.cuda_stream]  # noqa: E731
     torch.cuda.synchronize()
-    at, copy = marks.data_ptr(), torch.empty_like(marks)
+    torch.cuda.empty_cache()
+    st = next(s for s in (torch.cuda.Stream() for _ in range(64)) if not held(s))
+    marks = torch.full((size,), 5, dtype=torch.uint8, device="cuda")
+    copy = torch.empty_like(marks)
+    torch.cuda.synchronize()
     torch.cuda._sleep(2_000_000)  # the current stream is busy, its copy from `marks` yet to come
     copy.copy_(marks)
     del marks
     ops.m3_attn_prefix(q, pool, pages_t, f["prefix"], table_t, lens_t, out, lse, stream=st)
-    again = torch.empty(size, dtype=torch.uint8, device="cuda")
-    assert again.data_ptr() == at  # still the current stream's
+    assert held(st)  # the stream's own memory
     torch.cuda.synchronize()
     assert bool((copy == 5).all())
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
@@ -228,6 +230,20 @@ def test_prefix_workspace_of_a_captured_stream(ops, current):
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert all(bool((x == 5).all()) for x in taken)
+
+
+def test_prefix_on_the_default_stream_by_hand(ops):
+    f, (q, pool, pages, shared, table, own) = case_of("shared", 9)
+    want = run_prefix(ops, f, q, pool, pages, table)
+    pages_t, table_t, lens_t = i32(pages), i32(table), i32(f["lens"])
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        ops.m3_attn_prefix(q, pool, pages_t, f["prefix"], table_t, lens_t, out, lse, stream=torch.cuda.default_stream())
+        assert torch.cuda.current_stream() == other
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 # ----------------------------------------------------------------- rules ---
